@@ -18,7 +18,7 @@
  *  - A context belongs to the device that was current when it was created.
  *    The compute calls (tq_quantize, tq_decode_attention,
  *    tq_decode_attention_noalloc, tq_prefill_attention, tq_weight_quantize,
- *    tq_weight_gemm) check that this device is current and return
+ *    tq_weight_gemm, tq_build_tables) check that this device is current and return
  *    TQ_ERR_INVALID, launching nothing, when it is not.  One process may hold
  *    contexts on several devices.
  *  - The compute calls are asynchronous on the given stream (a cudaStream_t
@@ -324,6 +324,64 @@ tq_status tq_decode_attention_noalloc(tq_ctx *ctx, const tq_cache *cache,
                                       const int32_t *seq_lens,
                                       int32_t max_seq_len, float scale,
                                       float *out, float *lse, void *stream);
+
+/*
+ * The tables of one engine step, built on the device from request lengths
+ * (no counterpart in the method's sources: the step in front of tq_quantize
+ * and of the attention calls in a serving loop).  Sequence s holds
+ * cached_lens[s] tokens and gets new_lens[s] more (a whole prompt, a chunk,
+ * one token of a decode step, or none); the new tokens' rows are packed one
+ * sequence behind the other.  Written are
+ *  seq_idx, pos  device int32 [n_tok]: sequence and position of every new row,
+ *                as tq_quantize takes them;
+ *  slots         device int64 [n_tok] or NULL: the token's slot, block *
+ *                block_size + offset in a paged cache, s * capacity + pos in a
+ *                contiguous one (-1 where the token has no block);
+ *  cu_new        device int32 [n_seqs + 1]: first row of every sequence and
+ *                the total, as tq_prefill_attention (cu_q) and
+ *                tq_prompt_attention take them;
+ *  seq_lens      device int32 [n_seqs]: cached + new, as the attention calls
+ *                take them;
+ *  block_table   (paged cache; the writable pointer to cache->block_table's
+ *                memory) entry j of sequence s, for every block j with
+ *                ceil(cached / block_size) <= j < ceil((cached + new) /
+ *                block_size): the next block of the free list, sequence after
+ *                sequence.  Other entries stay as they are;
+ *  free_end      device int32 [1]: free_start plus the blocks taken.
+ * free_list: device int32 [n_free], physical blocks in the order they are
+ * given out; free_start: device int32 [1], how many of them are gone.
+ * Groups of sequences may share a prefix: the sequences cu_group[g] ..
+ * cu_group[g + 1] - 1 (device int32 [n_groups + 1], non-decreasing) begin with
+ * the same prefix_lens[g] tokens (device int32 [n_groups], multiples of
+ * block_size), and the first prefix_lens[g] / block_size entries of every
+ * member but the first become the first member's.  Such a member counts the
+ * prefix in its cached_lens.  n_groups = 0: none (cu_group and prefix_lens
+ * may be NULL); a contiguous cache has no table and ignores the groups.
+ * Of `cache` only n_seqs (at most 4096), capacity, block_table, block_size
+ * and n_blocks are used (n_kv_heads and the planes are not).  For a contiguous
+ * cache block_table is NULL and the free list's arguments are ignored.
+ * n_tok is the room in seq_idx, pos and slots; rows behind the last sequence's
+ * are left as they are.  No output may overlap an input or another output.
+ * Device-side errors are flagged (tq_check_device_errors) and handled so:
+ * a sequence with a negative length or more than capacity tokens gets none
+ * and seq_lens = 0 (bit 1); a prefix that is negative, no multiple of
+ * block_size, longer than the member's cached_lens or than the first member's
+ * tokens is not shared (bit 1); when the free list runs out, or an entry lies
+ * outside [0, n_blocks), the table entry and the slots become -1, free_end at
+ * most n_free (bit 0); rows past n_tok are not written (bit 0).
+ * The same call on the same inputs writes the same outputs, so a captured
+ * call may be replayed.  Asynchronous on `stream`, one kernel, allocates
+ * nothing.  Errors: TQ_ERR_INVALID, TQ_ERR_UNSUPPORTED (n_seqs), TQ_ERR_CUDA.
+ */
+tq_status tq_build_tables(tq_ctx *ctx, const tq_cache *cache,
+                          int32_t *block_table, const int32_t *cached_lens,
+                          const int32_t *new_lens, const int32_t *free_list,
+                          int32_t n_free, const int32_t *free_start,
+                          int32_t *free_end, const int32_t *cu_group,
+                          const int32_t *prefix_lens, int32_t n_groups,
+                          int32_t n_tok, int32_t *seq_idx, int32_t *pos,
+                          int64_t *slots, int32_t *cu_new, int32_t *seq_lens,
+                          void *stream);
 
 /*
  * Synchronise `stream`, then report and clear the context's sticky

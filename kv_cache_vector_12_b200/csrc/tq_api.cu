@@ -110,19 +110,13 @@ tq_status check_params(int d, int bits_k, int bits_v, int qjl, int law) {
   return TQ_OK;
 }
 
-tq_status check_cache(const tq_ctx *ctx, const tq_cache *c) {
+// The cache's sizes and layout, without its planes.
+tq_status check_geometry(const tq_cache *c) {
   if (!c) return fail(TQ_ERR_INVALID, "cache is NULL");
   if (c->capacity <= 0 || c->capacity % 64 != 0)
     return fail(TQ_ERR_INVALID, "capacity=%d must be a positive multiple of 64", c->capacity);
   if (c->n_seqs <= 0 || c->n_kv_heads <= 0)
     return fail(TQ_ERR_INVALID, "n_seqs=%d n_kv_heads=%d must be positive", c->n_seqs, c->n_kv_heads);
-  const void *planes[6] = {c->codes_k, c->norm_k, c->qjl_bits, c->qjl_norm, c->codes_v, c->norm_v};
-  for (int i = 0; i < 6; ++i) {
-    const bool needed = (i != 2 && i != 3) || ctx->qjl;
-    if (needed && !planes[i]) return fail(TQ_ERR_INVALID, "cache plane %d is NULL", i);
-    if (planes[i] && !aligned16(planes[i]))
-      return fail(TQ_ERR_INVALID, "cache plane %d is not 16-byte aligned", i);
-  }
   if (c->block_table) {  // paged layout
     if (((uintptr_t)c->block_table & 3u) != 0) return fail(TQ_ERR_INVALID, "block_table must be 4-byte aligned");
     if (c->block_size <= 0 || c->block_size % 64 != 0)
@@ -130,6 +124,25 @@ tq_status check_cache(const tq_ctx *ctx, const tq_cache *c) {
     if (c->capacity % c->block_size != 0)
       return fail(TQ_ERR_INVALID, "capacity=%d must be a multiple of block_size=%d", c->capacity, c->block_size);
     if (c->n_blocks <= 0) return fail(TQ_ERR_INVALID, "n_blocks=%d must be positive", c->n_blocks);
+  }
+  return TQ_OK;
+}
+
+// Whether [a, a + na) and [b, b + nb) share a byte (a NULL pointer is no range).
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+tq_status check_cache(const tq_ctx *ctx, const tq_cache *c) {
+  const tq_status st = check_geometry(c);
+  if (st != TQ_OK) return st;
+  const void *planes[6] = {c->codes_k, c->norm_k, c->qjl_bits, c->qjl_norm, c->codes_v, c->norm_v};
+  for (int i = 0; i < 6; ++i) {
+    const bool needed = (i != 2 && i != 3) || ctx->qjl;
+    if (needed && !planes[i]) return fail(TQ_ERR_INVALID, "cache plane %d is NULL", i);
+    if (planes[i] && !aligned16(planes[i]))
+      return fail(TQ_ERR_INVALID, "cache plane %d is not 16-byte aligned", i);
   }
   return TQ_OK;
 }
@@ -155,7 +168,7 @@ tq_status check_context_device(const tq_ctx *ctx) {
 }
 
 // Cached once per device (atomically: calls may come from several threads).
-static int sm_count() {
+int sm_count() {
   static std::atomic<int> cached[kMaxDevices];
   const int dev = current_device();
   int n = cached[dev].load(std::memory_order_relaxed);
@@ -637,6 +650,70 @@ tq_status tq_weight_gemm(tq_ctx *ctx, const tq_cache *w, int32_t n_out, int32_t 
   if (workspace_bytes < need) return fail(TQ_ERR_INVALID, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
   const int e = tq::launch_weight_gemm(ctx->dp, *w, n_out, n_in, x, x_dtype, n_tok, y, (char *)workspace, stream);
   if (e != 0) return cuda_fail((cudaError_t)e, "tq_weight_gemm launch");
+  return TQ_OK;
+}
+
+tq_status tq_build_tables(tq_ctx *ctx, const tq_cache *cache, int32_t *block_table, const int32_t *cached_lens,
+                          const int32_t *new_lens, const int32_t *free_list, int32_t n_free,
+                          const int32_t *free_start, int32_t *free_end, const int32_t *cu_group,
+                          const int32_t *prefix_lens, int32_t n_groups, int32_t n_tok, int32_t *seq_idx, int32_t *pos,
+                          int64_t *slots, int32_t *cu_new, int32_t *seq_lens, void *stream) {
+  if (!ctx) return fail(TQ_ERR_INVALID, "ctx is NULL");
+  tq_status st = tq::check_context_device(ctx);
+  if (st != TQ_OK) return st;
+  st = check_geometry(cache);
+  if (st != TQ_OK) return st;
+  if (cache->n_seqs > tq::kMaxTableSeqs)
+    return fail(TQ_ERR_UNSUPPORTED, "n_seqs=%d > %d", cache->n_seqs, tq::kMaxTableSeqs);
+  if ((block_table != nullptr) != (cache->block_table != nullptr))
+    return fail(TQ_ERR_INVALID, "block_table must be given for a paged cache and NULL for a contiguous one");
+  if (!cached_lens || !new_lens || !cu_new || !seq_lens)
+    return fail(TQ_ERR_INVALID, "cached_lens, new_lens, cu_new and seq_lens must be non-NULL");
+  if (n_tok < 0) return fail(TQ_ERR_INVALID, "n_tok=%d is negative", n_tok);
+  if (n_tok > 0 && (!seq_idx || !pos)) return fail(TQ_ERR_INVALID, "seq_idx and pos must be non-NULL");
+  if (n_groups < 0 || n_groups > cache->n_seqs)
+    return fail(TQ_ERR_INVALID, "n_groups=%d outside [0, n_seqs=%d]", n_groups, cache->n_seqs);
+  if (n_groups > 0 && (!cu_group || !prefix_lens))
+    return fail(TQ_ERR_INVALID, "cu_group and prefix_lens must be non-NULL with n_groups=%d", n_groups);
+  if (block_table && (n_free < 0 || (n_free > 0 && !free_list) || !free_start || !free_end))
+    return fail(TQ_ERR_INVALID, "a paged cache needs n_free >= 0 free blocks, free_start and free_end");
+  const void *words[] = {block_table, cached_lens, new_lens, free_list, free_start, free_end,
+                         cu_group,    prefix_lens, seq_idx,  pos,       cu_new,     seq_lens};
+  for (const void *w : words)
+    if ((uintptr_t)w & 3u) return fail(TQ_ERR_INVALID, "an int32 array is not 4-byte aligned");
+  if ((uintptr_t)slots & 7u) return fail(TQ_ERR_INVALID, "slots must be 8-byte aligned");
+  // Every CTA reads the inputs on its own, so no output may lie over one.
+  const size_t n = (size_t)cache->n_seqs;
+  struct Range {
+    const void *p;
+    size_t bytes;
+  };
+  const Range in[] = {{cached_lens, 4 * n},
+                      {new_lens, 4 * n},
+                      {block_table ? free_list : nullptr, 4 * (size_t)(n_free > 0 ? n_free : 0)},
+                      {block_table ? free_start : nullptr, 4},
+                      {n_groups ? cu_group : nullptr, 4 * ((size_t)n_groups + 1)},
+                      {n_groups ? prefix_lens : nullptr, 4 * (size_t)n_groups}};
+  const Range out[] = {{block_table, block_table ? 4 * n * (size_t)(cache->capacity / cache->block_size) : 0},
+                       {block_table ? free_end : nullptr, 4},
+                       {seq_idx, 4 * (size_t)n_tok},
+                       {pos, 4 * (size_t)n_tok},
+                       {slots, 8 * (size_t)n_tok},
+                       {cu_new, 4 * (n + 1)},
+                       {seq_lens, 4 * n}};
+  const int n_out = (int)(sizeof out / sizeof out[0]);
+  for (int i = 0; i < n_out; ++i) {
+    for (const Range &r : in)
+      if (overlap(out[i].p, out[i].bytes, r.p, r.bytes))
+        return fail(TQ_ERR_INVALID, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+        return fail(TQ_ERR_INVALID, "two outputs overlap");
+  }
+  const int e = tq::launch_tables(ctx->dp, *cache, block_table, cached_lens, new_lens, free_list, n_free, free_start,
+                                  free_end, cu_group, prefix_lens, n_groups, n_tok, seq_idx, pos, slots, cu_new,
+                                  seq_lens, stream);
+  if (e != 0) return cuda_fail((cudaError_t)e, "tq_build_tables launch");
   return TQ_OK;
 }
 

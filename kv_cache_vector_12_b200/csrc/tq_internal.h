@@ -112,6 +112,8 @@ tq_status check_context_device(const tq_ctx *ctx);
 constexpr int kMaxDevices = 64;
 // The current device's ordinal, clamped into [0, kMaxDevices).
 int current_device();
+// SMs of the current device (tq_api.cu).
+int sm_count();
 
 // --- launches (tq_kernels.cu, tq_decode.cu); return a cudaError_t as int ---
 int launch_quantize(const DeviceParams &p, const tq_cache &c, const void *k, const void *v,
@@ -155,6 +157,12 @@ int launch_prefill(const DeviceParams &p, const tq_cache &c, const void *q, int 
 size_t weight_workspace_bytes(int n_tok, int n_in);
 int launch_weight_gemm(const DeviceParams &p, const tq_cache &w, int n_out, int n_in, const void *x, int x_dtype,
                        int n_tok, float *y, char *workspace, void *stream);
+// Tables of one engine step from request lengths (tq_tables.cu).
+constexpr int kMaxTableSeqs = 4096;  // the kernel's two sums of every sequence in 32 KB of shared memory
+int launch_tables(const DeviceParams &p, const tq_cache &c, int32_t *block_table, const int32_t *cached,
+                  const int32_t *fresh, const int32_t *free_list, int n_free, const int32_t *free_start,
+                  int32_t *free_end, const int32_t *cu_group, const int32_t *prefix, int n_groups, int n_tok,
+                  int32_t *seq_idx, int32_t *pos, int64_t *slots, int32_t *cu_new, int32_t *seq_lens, void *stream);
 int launch_decode(const DeviceParams &p, const tq_cache &c, const void *q, int q_dtype,
                   int n_q_heads, const int32_t *seq_lens, int max_seq_len, float scale,
                   float *out, float *lse, char *workspace, const DecodeSplit &split,

@@ -69,6 +69,9 @@ lib.tq_weight_workspace_bytes.restype = ctypes.c_size_t
 lib.tq_weight_gemm.argtypes = [_vp, ctypes.POINTER(tq_cache), _i32, _i32, _vp, _i32, _i32, _vp, _vp,
                                ctypes.c_size_t, _vp]
 lib.tq_weight_gemm.restype = ctypes.c_int
+lib.tq_build_tables.argtypes = [_vp, ctypes.POINTER(tq_cache), _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32,
+                                _i32, _vp, _vp, _vp, _vp, _vp, _vp]
+lib.tq_build_tables.restype = ctypes.c_int
 lib.tq_check_device_errors.argtypes = [_vp, _vp]
 lib.tq_check_device_errors.restype = ctypes.c_int
 lib.tq_last_error.argtypes = []
@@ -271,6 +274,26 @@ def decode_attention_noalloc(ctx: Context, cache: Cache, q: torch.Tensor, seq_le
     _check(lib.tq_decode_attention_noalloc(ctx.handle, ctypes.byref(cache.struct), _ptr(q), q_dtype, q.shape[1],
                                            _ptr(seq_lens), max_seq_len, scale, _ptr(out), _ptr(lse),
                                            _stream(stream)))
+
+
+def build_tables(ctx: Context, cache: Cache, cached_lens: torch.Tensor, new_lens: torch.Tensor, seq_idx: torch.Tensor,
+                 pos: torch.Tensor, cu_new: torch.Tensor, seq_lens: torch.Tensor, slots: torch.Tensor | None = None,
+                 free_list: torch.Tensor | None = None, free_start: torch.Tensor | None = None,
+                 free_end: torch.Tensor | None = None, cu_group: torch.Tensor | None = None,
+                 prefix_lens: torch.Tensor | None = None, stream=None) -> None:
+    """tq_build_tables: seq_idx, pos (int32 [n_tok]), slots (int64 [n_tok] or
+    None), cu_new (int32 [n_seqs + 1]) and seq_lens (int32 [n_seqs]) of one
+    engine step from cached_lens and new_lens (int32 [n_seqs]).  A PagedCache's
+    own block table gets the new blocks from free_list (int32), starting at
+    free_start (int32 [1]); free_end (int32 [1]) is where the next step
+    starts.  cu_group (int32 [n_groups + 1]) and prefix_lens (int32
+    [n_groups]): groups of sequences that begin with the same blocks."""
+    table = getattr(cache, "block_table", None)
+    _check(lib.tq_build_tables(ctx.handle, ctypes.byref(cache.struct), _ptr(table), _ptr(cached_lens),
+                               _ptr(new_lens), _ptr(free_list), 0 if free_list is None else free_list.numel(),
+                               _ptr(free_start), _ptr(free_end), _ptr(cu_group), _ptr(prefix_lens),
+                               0 if prefix_lens is None else prefix_lens.numel(), seq_idx.numel(), _ptr(seq_idx),
+                               _ptr(pos), _ptr(slots), _ptr(cu_new), _ptr(seq_lens), _stream(stream)))
 
 
 class WeightCache:
