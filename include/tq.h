@@ -18,7 +18,7 @@
  *  - A context belongs to the device that was current when it was created.
  *    The compute calls (tq_quantize, tq_decode_attention,
  *    tq_decode_attention_noalloc, tq_prefill_attention, tq_weight_quantize,
- *    tq_weight_gemm, tq_build_tables) check that this device is current and return
+ *    tq_weight_gemm, tq_prompt_attention, tq_build_tables) check that this device is current and return
  *    TQ_ERR_INVALID, launching nothing, when it is not.  One process may hold
  *    contexts on several devices.
  *  - The compute calls are asynchronous on the given stream (a cudaStream_t
@@ -324,6 +324,43 @@ tq_status tq_decode_attention_noalloc(tq_ctx *ctx, const tq_cache *cache,
                                       const int32_t *seq_lens,
                                       int32_t max_seq_len, float scale,
                                       float *out, float *lse, void *stream);
+
+/*
+ * Causal attention over whole prompts before they are packed: q, k and v are
+ * the bf16 rows of n_seqs prompts, one behind the other, and every token
+ * attends over the tokens of its own prompt up to and including itself,
+ *   o_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j,
+ * query head g reading KV head g / (n_q_heads / n_kv_heads).  The exact
+ * counterpart of tq_prefill_attention (which reads the packed codes): a
+ * serving loop runs it on the same k and v that it hands to tq_quantize for
+ * the decode that follows.  The context gives d (64, 128 or 256) and the
+ * device; its bit widths and qjl play no part.
+ *  q, k, v     device bf16 [n_tok][heads][d] with q_stride, k_stride, v_stride
+ *              elements from one token to the next (the heads of a token are
+ *              contiguous): multiples of 8, at least heads * d, so the rows of
+ *              a fused projection are taken as they are.
+ *  cu_seqlens  device int32 [n_seqs + 1], non-decreasing, at most n_tok:
+ *              prompt s is tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1
+ *              (none is allowed).
+ *  max_len     host bound on every prompt's length (sizes the grid).
+ *  out         device [n_tok][n_q_heads][d] of out_dtype (TQ_BF16 or TQ_F32),
+ *              lse device fp32 [n_tok][n_q_heads] or NULL.  Tokens outside
+ *              every prompt are neither read for another's result nor written.
+ * scale <= 0 means 1/sqrt(d).  No workspace.  Query heads per KV head at most
+ * 16.  Scores and sums are fp32; the softmax weights are rounded to bf16 for
+ * the product with V.  A NaN or infinity in a token's K or V reaches, besides
+ * the queries at and after it, at most those up to 127 positions before it in
+ * the same prompt.  A prompt whose bounds are out of range or longer than
+ * max_len gets no output and sets the seq_len flag of tq_check_device_errors.
+ */
+tq_status tq_prompt_attention(tq_ctx *ctx, const void *q, const void *k,
+                              const void *v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride,
+                              int32_t n_tok, int32_t n_q_heads,
+                              int32_t n_kv_heads, const int32_t *cu_seqlens,
+                              int32_t n_seqs, int32_t max_len, float scale,
+                              void *out, int32_t out_dtype, float *lse,
+                              void *stream);
 
 /*
  * The tables of one engine step, built on the device from request lengths

@@ -653,6 +653,45 @@ tq_status tq_weight_gemm(tq_ctx *ctx, const tq_cache *w, int32_t n_out, int32_t 
   return TQ_OK;
 }
 
+tq_status tq_prompt_attention(tq_ctx *ctx, const void *q, const void *k, const void *v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int32_t n_tok, int32_t n_q_heads,
+                              int32_t n_kv_heads, const int32_t *cu_seqlens, int32_t n_seqs, int32_t max_len,
+                              float scale, void *out, int32_t out_dtype, float *lse, void *stream) {
+  if (!ctx) return fail(TQ_ERR_INVALID, "ctx is NULL");
+  tq_status st = tq::check_context_device(ctx);
+  if (st != TQ_OK) return st;
+  if (n_tok < 0 || n_seqs < 0) return fail(TQ_ERR_INVALID, "n_tok=%d n_seqs=%d is negative", n_tok, n_seqs);
+  if (max_len < 0 || max_len > n_tok) return fail(TQ_ERR_INVALID, "max_len=%d outside [0, n_tok=%d]", max_len, n_tok);
+  if (n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads != 0)
+    return fail(TQ_ERR_INVALID, "n_q_heads=%d must be a positive multiple of n_kv_heads=%d", n_q_heads, n_kv_heads);
+  if (n_q_heads / n_kv_heads > 16)
+    return fail(TQ_ERR_UNSUPPORTED, "query heads per KV head = %d > 16", n_q_heads / n_kv_heads);
+  if (n_kv_heads > 65535) return fail(TQ_ERR_UNSUPPORTED, "n_kv_heads=%d > 65535", n_kv_heads);
+  if (out_dtype != TQ_BF16 && out_dtype != TQ_F32) return fail(TQ_ERR_INVALID, "out_dtype=%d", out_dtype);
+  if (!std::isfinite(scale)) return fail(TQ_ERR_INVALID, "scale is not finite");
+  if (n_tok == 0 || n_seqs == 0 || max_len == 0) return TQ_OK;
+  if (!q || !k || !v || !cu_seqlens || !out)
+    return fail(TQ_ERR_INVALID, "q, k, v, cu_seqlens and out must be non-NULL");
+  const struct {
+    const char *name;
+    int64_t stride;
+    int heads;
+  } rows[] = {{"q", q_stride, n_q_heads}, {"k", k_stride, n_kv_heads}, {"v", v_stride, n_kv_heads}};
+  for (const auto &r : rows)  // (a tensor map's strides stay below 2^40 bytes)
+    if (r.stride < (int64_t)r.heads * ctx->d || r.stride % 8 != 0 || r.stride >= (int64_t)1 << 38)
+      return fail(TQ_ERR_INVALID, "%s_stride=%lld must be a multiple of 8, at least heads * d = %lld", r.name,
+                  (long long)r.stride, (long long)r.heads * ctx->d);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || ((uintptr_t)cu_seqlens & 3u) ||
+      (lse && ((uintptr_t)lse & 3u)))
+    return fail(TQ_ERR_INVALID, "misaligned q/k/v/out (16 B) or cu_seqlens/lse (4 B)");
+  if (scale <= 0.f) scale = 1.0f / std::sqrt((float)ctx->d);
+  const int e = tq::launch_prompt(ctx->dp, q, k, v, (long)q_stride, (long)k_stride, (long)v_stride, n_tok, n_q_heads,
+                                  n_kv_heads, cu_seqlens, n_seqs, max_len, scale, out, out_dtype == TQ_F32, lse,
+                                  stream);
+  if (e != 0) return cuda_fail((cudaError_t)e, "tq_prompt_attention launch");
+  return TQ_OK;
+}
+
 tq_status tq_build_tables(tq_ctx *ctx, const tq_cache *cache, int32_t *block_table, const int32_t *cached_lens,
                           const int32_t *new_lens, const int32_t *free_list, int32_t n_free,
                           const int32_t *free_start, int32_t *free_end, const int32_t *cu_group,

@@ -157,6 +157,11 @@ int launch_prefill(const DeviceParams &p, const tq_cache &c, const void *q, int 
 size_t weight_workspace_bytes(int n_tok, int n_in);
 int launch_weight_gemm(const DeviceParams &p, const tq_cache &w, int n_out, int n_in, const void *x, int x_dtype,
                        int n_tok, float *y, char *workspace, void *stream);
+// Causal attention over packed bf16 prompts (tq_prompt.cu); strides in
+// elements between tokens.
+int launch_prompt(const DeviceParams &p, const void *q, const void *k, const void *v, long q_stride, long k_stride,
+                  long v_stride, int n_tok, int n_q_heads, int n_kv_heads, const int32_t *cu, int n_seqs, int max_len,
+                  float scale, void *out, bool out_f32, float *lse, void *stream);
 // Tables of one engine step from request lengths (tq_tables.cu).
 constexpr int kMaxTableSeqs = 4096;  // the kernel's two sums of every sequence in 32 KB of shared memory
 int launch_tables(const DeviceParams &p, const tq_cache &c, int32_t *block_table, const int32_t *cached,

@@ -1,0 +1,611 @@
+// Causal attention over whole bf16 prompts packed one behind the other,
+// grouped query heads, sm_100a: the exact attention of a prompt's own tokens,
+// the step a serving loop runs beside tq_quantize (which packs the same K and
+// V for the decode that follows).
+//
+//   o_i = sum_{j <= i} p_ij v_j / l_i,  p_ij = 2^(c q_i . k_j - r_i),
+//   l_i = sum_{j <= i} p_ij,            c = scale log2(e),
+//   lse_i = ln 2 (r_i + log2 l_i)
+// with r_i a running reference: the row's maximum when it was last moved.
+// Keys are taken in tiles; r_i moves only when a tile's maximum passes it by
+// more than kLazy (so p <= 2^kLazy, far below the range of bf16 and fp32),
+// which makes rescaling O rare: after the first tiles almost no row moves.
+//
+// A CTA takes NT tiles of 128 query rows of one KV head (a row is one
+// (position, query head) pair: with G heads per KV head a tile holds 128 / G
+// positions, so K and V are read once for the whole group and a prompt of one
+// token still fills G rows) against the keys at or before them:
+//   producer  (1 thread)  Q once, then K and V tiles by TMA into a ring of
+//             128-byte-swizzled slots;
+//   MMA       (1 thread)  S = Q K^T, then O += P V with P as the A operand in
+//             tensor memory and V read from its token-major tile as an
+//             MN-major B operand (no transpose anywhere);
+//   softmax   (4 warps per row tile, one thread per row)  S from tensor
+//             memory, mask on diagonal tiles only, exp2, P as bf16 back into
+//             tensor memory, and at the end O / l to global memory.
+// With two row tiles (d = 64 and 128) the MMAs of one run under the softmax
+// of the other; at d = 256 one row tile fills tensor memory and S is
+// double-buffered over tiles of 64 keys instead.
+// P is rounded to bf16, V's type (one MMA takes one type for A and B); l is
+// summed in fp32 from the unrounded weights.
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <cmath>
+
+#include "tq_tc.cuh"
+
+namespace tq {
+namespace {
+
+constexpr float kLazy = 8.f;  // log2 units a tile's maximum may pass the reference
+
+template <int DH>
+struct PromptCfg {
+  static constexpr int NT = DH == 256 ? 1 : 2;      // row tiles of 128
+  static constexpr int KT = DH == 256 ? 64 : 128;   // keys per tile
+  static constexpr int kBoxes = DH / 64;            // 64-column swizzled boxes per operand
+  static constexpr int kQBox = 128 * 128;           // bytes of one box of a Q tile
+  static constexpr int kKVBox = KT * 128;           // bytes of one box of a K or V tile
+  static constexpr int kQTile = kBoxes * kQBox;
+  static constexpr int kSlot = kBoxes * kKVBox;
+  static constexpr int kSlots = DH == 64 ? 8 : 5;
+  static constexpr int kSoftWarps = 4 * NT;
+  static constexpr int kProdWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+  static constexpr int kThreads = 32 * (kSoftWarps + 2);
+  static constexpr int smem = 1024 + NT * kQTile + kSlots * kSlot;
+  // tensor-memory columns: S (P overwrites it when NT == 2) and O
+  static constexpr uint32_t s_col(int i) { return NT == 2 ? 128u * i : 256u + 64u * i; }
+  static constexpr uint32_t p_col(int i) { return NT == 2 ? 128u * i : 384u + 32u * i; }
+  static constexpr uint32_t o_col(int i) { return NT == 2 ? 256u + (uint32_t)DH * i : 0u; }
+  // instruction descriptors, kind::f16: bf16 A and B, fp32 D, M = 128; S has
+  // both operands K-major, O has B MN-major (bit 16)
+  static constexpr uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
+  static constexpr uint32_t idesc_s = base | ((uint32_t)(KT >> 3) << 17);
+  static constexpr uint32_t idesc_o = base | (1u << 16) | ((uint32_t)(DH >> 3) << 17);
+};
+
+struct PromptArgs {
+  unsigned *err;
+  const int32_t *cu;
+  int n_seqs, n_tok, max_len;
+  int n_q_heads, n_kv_heads, per_tile;  // positions per row tile
+  float c;                              // scale log2(e)
+  void *out;                            // [n_tok][n_q_heads][d], bf16 or fp32
+  bool out_f32;
+  float *lse;                           // [n_tok][n_q_heads] or null
+};
+
+// MN-major shared-memory descriptor of V: 128-byte swizzle, 64-column blocks
+// `block` bytes apart, groups of eight tokens 1024 bytes apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t block) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// D += A B with A in tensor memory and B in shared memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// 32 consecutive 32-bit columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// After ld_wait: passes the loaded registers through an empty asm, so that no
+// use of them is scheduled above the wait.
+__device__ __forceinline__ void pin32(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 16)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
+                 "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float f(uint32_t x) { return __uint_as_float(x); }
+
+// A bounded wait; false (the error flagged, the kernel told to stop) once it
+// expires.
+__device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, unsigned *err, int *stop) {
+  if (bar_wait(smem_addr(bar), parity)) return true;
+  atomicOr(err, kErrWaitExpired);
+  *(volatile int *)stop = 1;
+  return false;
+}
+
+// Query blocks (of `span` positions) of sequence s; 0 for a sequence outside
+// the call's bounds.
+__device__ __forceinline__ int blocks_of_seq(const PromptArgs &a, int s, int span, bool &bad) {
+  const int b = a.cu[s], e = a.cu[s + 1];
+  bad = b < 0 || e < b || e > a.n_tok || e - b > a.max_len;
+  return bad ? 0 : (e - b + span - 1) / span;
+}
+
+// The sequence and query block of CTA x, by one warp; s = -1 when there is
+// none.  Blocks with more keys come first, so that the last CTAs to start are
+// the shortest: within a sequence from its end, and with at most 32 sequences
+// (one per lane) across them too.  F(L) = sum_s max(0, blocks_s - L) blocks lie
+// at level L or above; the CTA's level is the largest L with F(L) > x.
+__device__ __forceinline__ void find_block(const PromptArgs &a, int span, int x, int lane, int &s, int &blk) {
+  s = -1;
+  blk = 0;
+  bool bad = false, any_bad = false;
+  if (a.n_seqs <= 32) {
+    const int nb = lane < a.n_seqs ? blocks_of_seq(a, lane, span, bad) : 0;
+    any_bad = bad;
+    const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)nb);
+    if ((unsigned)x < total) {
+      int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)nb);  // F(lo) > x >= F(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__reduce_add_sync(0xffffffffu, (unsigned)max(0, nb - mid)) > (unsigned)x) lo = mid;
+        else hi = mid;
+      }
+      // the blocks above level lo come first; this is the k-th sequence that reaches it
+      const int k = x - (int)__reduce_add_sync(0xffffffffu, (unsigned)max(0, nb - lo - 1));
+      const unsigned reach = __ballot_sync(0xffffffffu, nb > lo);
+      s = __fns(reach, 0, k + 1);
+      blk = lo;
+    }
+  } else {
+    int done = 0;  // blocks of the sequences before s0
+    for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
+      const int i = s0 + lane;
+      bad = false;
+      const int nb = i < a.n_seqs ? blocks_of_seq(a, i, span, bad) : 0;
+      any_bad |= bad;
+      int inc = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, done + inc > x);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        s = s0 + l;
+        blk = done + __shfl_sync(0xffffffffu, inc, l) - 1 - x;  // from the sequence's end
+        break;
+      }
+      done += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  if (any_bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrSeqLen);
+}
+
+template <int DH>
+__global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
+    prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v) {
+  using C = PromptCfg<DH>;
+  constexpr int NT = C::NT, KT = C::KT;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char *ring = sm + NT * C::kQTile;
+  __shared__ __align__(8) uint64_t q_full, full[C::kSlots], empty[C::kSlots];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], fin;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int stop, s_seq, s_blk;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+  const int G = a.n_q_heads / a.n_kv_heads, PC = a.per_tile, span = NT * PC;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) {
+    int s, blk;
+    find_block(a, span, blockIdx.x, lane, s, blk);
+    if (lane == 0) {
+      s_seq = s;
+      s_blk = blk;
+      stop = 0;
+    }
+  } else if (warp == C::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp == C::kProdWarp && lane == 0) {
+    bar_init(smem_addr(&q_full), 1);
+    for (int i = 0; i < C::kSlots; ++i) {
+      bar_init(smem_addr(&full[i]), 1);
+      bar_init(smem_addr(&empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(smem_addr(&s_full[i]), 1);
+      bar_init(smem_addr(&p_full[i]), 128);
+      bar_init(smem_addr(&o_full[i]), 1);
+    }
+    bar_init(smem_addr(&fin), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int s = s_seq;
+
+  if (s >= 0) {
+    const int tok0 = a.cu[s], len = a.cu[s + 1] - tok0;
+    const int first = s_blk * span;                    // first query position
+    // keys at or before the last query of each row tile, and their tiles
+    int tiles[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int b = first + i * PC, e = min(len, b + PC);
+      tiles[i] = e > b ? (e + KT - 1) / KT : 0;
+    }
+    const int n_tiles = NT == 2 ? max(tiles[0], tiles[1]) : tiles[0];
+
+    if (warp == C::kProdWarp) {
+      // ---------------- producer
+      if (lane == 0) {
+        const uint32_t box = (uint32_t)(PC * G * 128);
+        bar_expect_tx(smem_addr(&q_full), (NT == 2 && tiles[1] ? 2 : 1) * C::kBoxes * box);
+        for (int i = 0; i < NT; ++i)
+          if (tiles[i])
+            for (int b = 0; b < C::kBoxes; ++b)
+              tma_load_3d(smem_addr(sm + i * C::kQTile + b * C::kQBox), &map_q, 64 * b, h * G, tok0 + first + i * PC,
+                          smem_addr(&q_full));
+        int issued = 0;
+        for (int it = 0; it < 2 * n_tiles; ++it) {  // K 0, V 0, K 1, V 1, ...
+          const int slot = it % C::kSlots, use = it / C::kSlots;
+          if (use > 0 && !wait_or_stop(&empty[slot], (use - 1) & 1, a.err, &stop)) break;
+          if (*(volatile int *)&stop) break;
+          bar_expect_tx(smem_addr(&full[slot]), C::kSlot);
+          for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(smem_addr(ring + slot * C::kSlot + b * C::kKVBox), (it & 1) ? &map_v : &map_k, 64 * b, h,
+                        tok0 + (it >> 1) * KT, smem_addr(&full[slot]));
+          issued = it + 1;
+        }
+        if (*(volatile int *)&stop) {  // never leave copies in flight
+          bar_wait(smem_addr(&q_full), 0);
+          for (int it = max(0, issued - C::kSlots); it < issued; ++it)
+            bar_wait(smem_addr(&full[it % C::kSlots]), (it / C::kSlots) & 1);
+        }
+      }
+    } else if (warp == C::kMmaWarp) {
+      // ---------------- MMA issuer
+      if (lane == 0) {
+        auto slot_addr = [&](int it) { return smem_addr(ring + (it % C::kSlots) * C::kSlot); };
+        auto loaded = [&](int it) {
+          return wait_or_stop(&full[it % C::kSlots], (it / C::kSlots) & 1, a.err, &stop);
+        };
+        auto scores = [&](int i, int buf, int j) {  // row tile i, tensor-memory buffer buf, key tile j
+          const uint32_t q = smem_addr(sm + i * C::kQTile), k = slot_addr(2 * j);
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk)
+            tc_mma_n(tmem + C::s_col(buf), sw128_desc(q + (kk >> 2) * C::kQBox + (kk & 3) * 32),
+                     sw128_desc(k + (kk >> 2) * C::kKVBox + (kk & 3) * 32), C::idesc_s, kk > 0);
+        };
+        auto values = [&](int i, int buf, int j) {
+          const uint32_t v = slot_addr(2 * j + 1);
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            mma_ts(tmem + C::o_col(i), tmem + C::p_col(buf) + 8 * kk, mn_desc(v + kk * 2048, C::kKVBox), C::idesc_o,
+                   (j > 0 || kk > 0) ? 1u : 0u);
+        };
+        bool ok = wait_or_stop(&q_full, 0, a.err, &stop) && loaded(0);
+        if (ok) {
+          tc_fence_after();
+          if constexpr (NT == 2) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (tiles[i] > 0) {
+                scores(i, i, 0);
+                tc_commit(smem_addr(&s_full[i]));
+              }
+          } else {
+            scores(0, 0, 0);
+            tc_commit(smem_addr(&s_full[0]));
+          }
+          tc_commit(smem_addr(&empty[0]));
+        }
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          const bool more = j + 1 < n_tiles;
+          if constexpr (NT == 1) {
+            if (more) {
+              ok = loaded(2 * j + 2);
+              if (!ok || *(volatile int *)&stop) break;
+              // S and P buffer (j + 1) % 2 were last used by tile j - 1, whose
+              // weights were complete before its value MMAs were issued
+              scores(0, (j + 1) & 1, j + 1);
+              tc_commit(smem_addr(&s_full[(j + 1) & 1]));
+              tc_commit(smem_addr(&empty[(2 * j + 2) % C::kSlots]));
+            }
+            ok = loaded(2 * j + 1) && wait_or_stop(&p_full[j & 1], (j >> 1) & 1, a.err, &stop);
+            if (!ok || *(volatile int *)&stop) break;
+            tc_fence_after();
+            values(0, j & 1, j);
+            tc_commit(smem_addr(&o_full[0]));
+            if (!more) tc_commit(smem_addr(&o_full[1]));
+            tc_commit(smem_addr(&empty[(2 * j + 1) % C::kSlots]));
+          } else {
+            // O += P V of tile j, then S of tile j + 1 (over the P just read:
+            // MMAs of one thread run in order), for each row tile in turn
+            ok = loaded(2 * j + 1) && (!more || loaded(2 * j + 2));
+            if (!ok || *(volatile int *)&stop) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (j >= tiles[i]) continue;
+              ok = ok && wait_or_stop(&p_full[i], j & 1, a.err, &stop);
+              if (!ok) break;
+              tc_fence_after();
+              values(i, i, j);
+              if (j + 1 < tiles[i]) {
+                scores(i, i, j + 1);
+                tc_commit(smem_addr(&s_full[i]));
+              } else {
+                tc_commit(smem_addr(&o_full[i]));
+              }
+            }
+            if (!ok || *(volatile int *)&stop) break;
+            tc_commit(smem_addr(&empty[(2 * j + 1) % C::kSlots]));
+            if (more) tc_commit(smem_addr(&empty[(2 * j + 2) % C::kSlots]));
+          }
+        }
+        // every MMA issued here has completed before the tensor memory is released
+        tc_commit(smem_addr(&fin));
+        bar_wait(smem_addr(&fin), 0);
+      }
+    } else {
+      // ---------------- softmax: row tile i, one thread per row
+      const int i = NT == 2 ? warp >> 2 : 0, row = tid & 127;
+      const int n = tiles[i], base = first + i * PC;
+      const int t = row / G, pos = (row < PC * G && base + t < len) ? base + t : -1;
+      const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+      const uint32_t t_o = tmem + C::o_col(i) + lanes;
+      float ref = 0.f, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        const int buf = NT == 2 ? i : (j & 1);
+        const uint32_t par = NT == 2 ? (j & 1) : ((j >> 1) & 1);
+        ok = wait_or_stop(&s_full[buf], par, a.err, &stop);
+        if (!ok || *(volatile int *)&stop) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[KT / 32][32];
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) tmem_ld32(tmem + C::s_col(buf) + lanes + 32 * c, v[c]);
+        ld_wait();
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) pin32(v[c]);
+        const int key0 = j * KT;
+        if (key0 + KT - 1 > base) {  // some row of the tile does not see every key
+#pragma unroll
+          for (int c = 0; c < KT / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (key0 + 32 * c + e > pos) v[c][e] = 0xff800000u;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) mx = max3(mx, f(v[c][e]), f(v[c][e + 1]));
+        mx *= a.c;
+        if (j == 0) {
+          ref = fmaxf(mx, -3.0e38f);
+        } else {
+          // O may be rescaled as soon as the value MMAs of tile j - 1 are done
+          const bool move = mx > ref + kLazy;
+          if (__any_sync(0xffffffffu, move)) {
+            if constexpr (NT == 1) {
+              ok = wait_or_stop(&o_full[0], (j - 1) & 1, a.err, &stop);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const float nref = fmaxf(ref, mx), al = ex2(ref - nref);
+            ref = nref;
+            l *= al;
+#pragma unroll 1
+            for (int c = 0; c < DH / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(t_o + 32 * c, o);
+              ld_wait();
+              pin32(o);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float2 w = mul2(make_float2(f(o[e]), f(o[e + 1])), make_float2(al, al));
+                o[e] = __float_as_uint(w.x);
+                o[e + 1] = __float_as_uint(w.y);
+              }
+              tmem_st32(t_o + 32 * c, o);
+            }
+          }
+        }
+        const float2 c2 = make_float2(a.c, a.c), r2 = make_float2(-ref, -ref);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = fma2(make_float2(f(v[c][2 * e]), f(v[c][2 * e + 1])), c2, r2);
+            const float2 w = make_float2(ex2(x.x), ex2(x.y));
+            sum = add2(sum, w);
+            p[e] = pack_bf16(w.x, w.y);
+          }
+          tmem_st16(tmem + C::p_col(buf) + lanes + 16 * c, p);
+        }
+        l += sum.x + sum.y;
+        if (key0 + KT > len) {
+          // the tile's rows behind the sequence's end hold other tokens: zero
+          // them, so that a weight of 0 times what they hold stays 0
+          const int vs = 2 * j + 1;
+          ok = wait_or_stop(&full[vs % C::kSlots], (vs / C::kSlots) & 1, a.err, &stop);
+          if (!ok) break;
+          unsigned char *vt = ring + (vs % C::kSlots) * C::kSlot;
+          for (int x = 128 * (len - key0) + 16 * row; x < C::kKVBox; x += 128 * 16)
+#pragma unroll
+            for (int b = 0; b < C::kBoxes; ++b) *reinterpret_cast<uint4 *>(vt + b * C::kKVBox + x) = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        st_wait();
+        tc_fence_before();
+        bar_arrive(smem_addr(&p_full[buf]));
+      }
+      if (ok && n > 0) {
+        // (with NT == 1 o_full[0] takes a phase per tile, of which this thread
+        // may be two behind, so the last tile has a barrier of its own)
+        ok = wait_or_stop(&o_full[NT == 2 ? i : 1], 0, a.err, &stop);
+        if (ok) {
+          tc_fence_after();
+          const float il = 1.f / l;
+          const long orow = pos < 0 ? 0 : (long)(tok0 + pos) * a.n_q_heads + h * G + row % G;
+#pragma unroll 1
+          for (int c = 0; c < DH / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(t_o + 32 * c, o);
+            ld_wait();
+            pin32(o);
+            if (pos >= 0) {
+              if (a.out_f32) {
+                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * DH + 32 * c);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  dst[e] = make_float4(f(o[4 * e]) * il, f(o[4 * e + 1]) * il, f(o[4 * e + 2]) * il, f(o[4 * e + 3]) * il);
+              } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + orow * DH + 32 * c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  dst[e] = make_uint4(pack_bf16(f(o[8 * e]) * il, f(o[8 * e + 1]) * il),
+                                      pack_bf16(f(o[8 * e + 2]) * il, f(o[8 * e + 3]) * il),
+                                      pack_bf16(f(o[8 * e + 4]) * il, f(o[8 * e + 5]) * il),
+                                      pack_bf16(f(o[8 * e + 6]) * il, f(o[8 * e + 7]) * il));
+              }
+            }
+          }
+          if (a.lse && pos >= 0) a.lse[orow] = (ref + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+    }
+  }
+  // release the tensor memory once every MMA and tcgen05 access is finished
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// 3-D map over bf16 rows [tokens][heads][DH] with a token stride (elements),
+// boxes of 64 columns x box_heads x box_tokens, 128-byte swizzle.
+bool make_token_map(CUtensorMap *m, const void *base, int d, int heads, long tokens, long stride, int box_heads,
+                    int box_tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DH>
+int launch(const PromptArgs &args, const void *q, const void *k, const void *v, long qs, long ks, long vs,
+           void *stream) {
+  using C = PromptCfg<DH>;
+  const int G = args.n_q_heads / args.n_kv_heads;
+  CUtensorMap mq, mk, mv;
+  if (!make_token_map(&mq, q, DH, args.n_q_heads, args.n_tok, qs, G, args.per_tile) ||
+      !make_token_map(&mk, k, DH, args.n_kv_heads, args.n_tok, ks, 1, C::KT) ||
+      !make_token_map(&mv, v, DH, args.n_kv_heads, args.n_tok, vs, 1, C::KT))
+    return (int)cudaErrorInvalidValue;
+  static std::atomic<bool> configured[kMaxDevices];
+  std::atomic<bool> &done = configured[current_device()];
+  if (!done.load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+    if (e != cudaSuccess) return (int)e;
+    done.store(true, std::memory_order_release);
+  }
+  // at most this many query blocks, whatever the lengths
+  const long span = (long)C::NT * args.per_tile;
+  const long by_tok = (long)args.n_tok / span + args.n_seqs, by_len = (args.max_len + span - 1) / span * args.n_seqs;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(by_tok < by_len ? by_tok : by_len), args.n_kv_heads);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::smem;
+  cfg.stream = (cudaStream_t)stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, prompt_kernel<DH>, args, mq, mk, mv);
+}
+
+}  // namespace
+
+int launch_prompt(const DeviceParams &p, const void *q, const void *k, const void *v, long q_stride, long k_stride,
+                  long v_stride, int n_tok, int n_q_heads, int n_kv_heads, const int32_t *cu, int n_seqs, int max_len,
+                  float scale, void *out, bool out_f32, float *lse, void *stream) {
+  PromptArgs a{};
+  a.err = p.err;
+  a.cu = cu;
+  a.n_seqs = n_seqs;
+  a.n_tok = n_tok;
+  a.max_len = max_len;
+  a.n_q_heads = n_q_heads;
+  a.n_kv_heads = n_kv_heads;
+  a.per_tile = 128 / (n_q_heads / n_kv_heads);
+  a.c = scale * 1.4426950408889634f;
+  a.out = out;
+  a.out_f32 = out_f32;
+  a.lse = lse;
+  if (p.d == 64) return launch<64>(a, q, k, v, q_stride, k_stride, v_stride, stream);
+  if (p.d == 256) return launch<256>(a, q, k, v, q_stride, k_stride, v_stride, stream);
+  return launch<128>(a, q, k, v, q_stride, k_stride, v_stride, stream);
+}
+
+}  // namespace tq

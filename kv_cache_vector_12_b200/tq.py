@@ -69,6 +69,9 @@ lib.tq_weight_workspace_bytes.restype = ctypes.c_size_t
 lib.tq_weight_gemm.argtypes = [_vp, ctypes.POINTER(tq_cache), _i32, _i32, _vp, _i32, _i32, _vp, _vp,
                                ctypes.c_size_t, _vp]
 lib.tq_weight_gemm.restype = ctypes.c_int
+lib.tq_prompt_attention.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _i32, _i32, _i32,
+                                    _vp, _i32, _i32, ctypes.c_float, _vp, _i32, _vp, _vp]
+lib.tq_prompt_attention.restype = ctypes.c_int
 lib.tq_build_tables.argtypes = [_vp, ctypes.POINTER(tq_cache), _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32,
                                 _i32, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.tq_build_tables.restype = ctypes.c_int
@@ -274,6 +277,20 @@ def decode_attention_noalloc(ctx: Context, cache: Cache, q: torch.Tensor, seq_le
     _check(lib.tq_decode_attention_noalloc(ctx.handle, ctypes.byref(cache.struct), _ptr(q), q_dtype, q.shape[1],
                                            _ptr(seq_lens), max_seq_len, scale, _ptr(out), _ptr(lse),
                                            _stream(stream)))
+
+
+def prompt_attention(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     max_len: int, out: torch.Tensor, lse: torch.Tensor | None = None, scale: float = 0.0,
+                     stream=None) -> None:
+    """tq_prompt_attention: causal attention over prompts packed one behind the
+    other, prompt s being tokens cu_seqlens[s]:cu_seqlens[s+1]; q bf16 [n_tok,
+    n_q_heads, d], k and v bf16 [n_tok, n_kv_heads, d] (slices of one fused
+    projection are taken by their token stride); out bf16 or fp32 [n_tok,
+    n_q_heads, d], lse fp32 [n_tok, n_q_heads]."""
+    out_dtype = TQ_F32 if out.dtype == torch.float32 else TQ_BF16
+    _check(lib.tq_prompt_attention(ctx.handle, _ptr(q), _ptr(k), _ptr(v), q.stride(0), k.stride(0), v.stride(0),
+                                   q.shape[0], q.shape[1], k.shape[1], _ptr(cu_seqlens), cu_seqlens.numel() - 1,
+                                   max_len, scale, _ptr(out), out_dtype, _ptr(lse), _stream(stream)))
 
 
 def build_tables(ctx: Context, cache: Cache, cached_lens: torch.Tensor, new_lens: torch.Tensor, seq_idx: torch.Tensor,
