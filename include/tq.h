@@ -17,7 +17,8 @@
  *    buffer; the library never frees, keeps or allocates caller memory.
  *  - A context belongs to the device that was current when it was created.
  *    The compute calls (tq_quantize, tq_decode_attention,
- *    tq_decode_attention_noalloc, tq_prefill_attention, tq_weight_quantize,
+ *    tq_decode_attention_noalloc, tq_decode_attention_shared,
+ *    tq_prefill_attention, tq_weight_quantize,
  *    tq_weight_gemm, tq_prompt_attention, tq_build_tables) check that this device is current and return
  *    TQ_ERR_INVALID, launching nothing, when it is not.  One process may hold
  *    contexts on several devices.
@@ -324,6 +325,51 @@ tq_status tq_decode_attention_noalloc(tq_ctx *ctx, const tq_cache *cache,
                                       const int32_t *seq_lens,
                                       int32_t max_seq_len, float scale,
                                       float *out, float *lse, void *stream);
+
+/* Device workspace (bytes) that tq_decode_attention_shared needs for these
+ * sizes; 0 for sizes that the call refuses.  Of `cache` n_seqs, n_kv_heads and
+ * the layout are used; the context's device must be current. */
+size_t tq_shared_workspace_bytes(const tq_ctx *ctx, const tq_cache *cache,
+                                 int32_t n_q_heads, int32_t n_groups,
+                                 int32_t max_group, int32_t max_prefix_len,
+                                 int32_t max_suffix_len);
+
+/*
+ * tq_decode_attention for a batch whose sequences share long prefixes (a
+ * system prompt, several samples of one prompt): sequences cu_group[g] ..
+ * cu_group[g + 1] - 1 form group g, positions [0, prefix_lens[g]) of all of
+ * them are read from the group's first sequence, once for the whole group,
+ * and positions [prefix_lens[g], seq_lens[s]) from sequence s itself.  Scores,
+ * softmax and values are those of tq_decode_attention over the union.
+ *  cu_group     device int32 [n_groups + 1], cu_group[0] = 0, non-decreasing,
+ *               cu_group[n_groups] = n_seqs (a group may be empty or hold one
+ *               sequence).
+ *  prefix_lens  device int32 [n_groups], any length (no multiple of anything),
+ *               0 for a group that shares nothing.
+ *  seq_lens     device int32 [n_seqs]: the prefix included, so at least
+ *               prefix_lens of its group; or 0 for a sequence that takes no
+ *               part (out = 0, lse = -inf).  The first sequence of a group
+ *               holds the prefix whatever its own length.
+ *  max_group, max_prefix_len, max_suffix_len  host bounds on the group sizes,
+ *               prefix_lens and seq_lens - prefix_lens (they size the grid and
+ *               the workspace).
+ *  out          device [n_seqs][n_q_heads][d] of out_dtype (TQ_BF16 or
+ *               TQ_F32); the other arguments are tq_decode_attention's.
+ * In a contiguous cache the members' own positions below the prefix are not
+ * used, whatever they hold (those from the prefix rounded down to a multiple
+ * of 64 are read and masked).  In a paged cache a member's table is read from
+ * the block that holds the prefix's end on, and only if it has positions
+ * there; entries before it may hold anything.  A sequence outside every group,
+ * in a group of more than max_group, or with lengths outside the bounds gets out = 0, lse = -inf and sets the
+ * seq_len flag of tq_check_device_errors.
+ */
+tq_status tq_decode_attention_shared(
+    tq_ctx *ctx, const tq_cache *cache, const void *q, int32_t q_dtype,
+    int32_t n_q_heads, const int32_t *seq_lens, const int32_t *cu_group,
+    const int32_t *prefix_lens, int32_t n_groups, int32_t max_group,
+    int32_t max_prefix_len, int32_t max_suffix_len, float scale, void *out,
+    int32_t out_dtype, float *lse, void *workspace, size_t workspace_bytes,
+    void *stream);
 
 /*
  * Causal attention over whole prompts before they are packed: q, k and v are

@@ -20,14 +20,15 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtq.so")
 
-# (source, object name, extra flags): tq_decode_variants.cu is compiled once
-# per (head dimension, K width) slice of the attention kernel's instantiations
+# (source, object name, extra flags): tq_decode_variants.cu and
+# tq_shared_variants.cu are compiled once per (head dimension, K width) slice of
+# the attention kernel's instantiations
 SOURCES = [(s, os.path.splitext(s)[0], []) for s in
            ["tq_host.cpp", "tq_fragments.cpp", "tq_api.cu", "tq_kernels.cu", "tq_quantize_tc.cu",
             "tq_quantize_qjl_tc.cu", "tq_quantize_tc256.cu", "tq_decode.cu", "tq_prefill.cu", "tq_weight.cu",
-            "tq_noalloc.cu", "tq_tables.cu", "tq_prompt.cu"]]
-SOURCES += [("tq_decode_variants.cu", f"tq_decode_variants_d{d}_k{bk}", [f"-DTQ_DECODE_DH={d}", f"-DTQ_DECODE_BK={bk}"])
-            for d in (64, 128, 256) for bk in (2, 3, 4)]
+            "tq_noalloc.cu", "tq_tables.cu", "tq_prompt.cu", "tq_shared.cu"]]
+SOURCES += [(f"{name}.cu", f"{name}_d{d}_k{bk}", [f"-DTQ_DECODE_DH={d}", f"-DTQ_DECODE_BK={bk}"])
+            for name in ("tq_decode_variants", "tq_shared_variants") for d in (64, 128, 256) for bk in (2, 3, 4)]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "-I" + os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]

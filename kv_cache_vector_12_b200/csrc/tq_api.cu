@@ -466,6 +466,7 @@ tq_status tq_create_ex(tq_ctx **out, int32_t d, int32_t bits_k, int32_t bits_v, 
       tq::decode_ctas_per_sm(d, bits_k, bits_v, qjl, 8, long_splits, paged);
       tq::decode_ctas_per_sm(d, bits_k, bits_v, qjl, 16, long_splits, paged);
     }
+  for (const int nt : {1, 2}) tq::shared_ctas_per_sm(d, bits_k, bits_v, qjl, nt);
   *out = ctx;
   return TQ_OK;
 }
@@ -560,6 +561,81 @@ tq_status tq_decode_attention(tq_ctx *ctx, const tq_cache *cache, const void *q,
   const int e = tq::launch_decode(ctx->dp, *cache, q, q_dtype, n_q_heads, seq_lens, max_seq_len, scale,
                                   out, lse, (char *)workspace, sp, ws, stream);
   if (e != 0) return cuda_fail((cudaError_t)e, "tq_decode_attention launch");
+  return TQ_OK;
+}
+
+namespace {
+
+// Sizes of a shared-prefix call (the same for the workspace and the call).
+tq_status check_shared_sizes(const tq_cache *cache, int32_t n_q_heads, int32_t n_groups, int32_t max_group,
+                             int32_t max_prefix_len, int32_t max_suffix_len) {
+  if (n_q_heads <= 0 || n_q_heads % cache->n_kv_heads != 0)
+    return fail(TQ_ERR_INVALID, "n_q_heads=%d must be a positive multiple of n_kv_heads=%d", n_q_heads,
+                cache->n_kv_heads);
+  if (n_q_heads / cache->n_kv_heads > 16)
+    return fail(TQ_ERR_UNSUPPORTED, "query heads per KV head = %d > 16", n_q_heads / cache->n_kv_heads);
+  if (cache->n_seqs > 65535 || cache->n_kv_heads > 65535)
+    return fail(TQ_ERR_UNSUPPORTED, "n_seqs=%d n_kv_heads=%d: at most 65535", cache->n_seqs, cache->n_kv_heads);
+  if ((int64_t)cache->n_seqs * n_q_heads > INT32_MAX)
+    return fail(TQ_ERR_UNSUPPORTED, "n_seqs * n_q_heads = %lld does not fit 31 bits",
+                (long long)cache->n_seqs * n_q_heads);
+  if (n_groups <= 0 || n_groups > cache->n_seqs)
+    return fail(TQ_ERR_INVALID, "n_groups=%d outside [1, n_seqs=%d]", n_groups, cache->n_seqs);
+  if (max_group <= 0 || max_group > cache->n_seqs)
+    return fail(TQ_ERR_INVALID, "max_group=%d outside [1, n_seqs=%d]", max_group, cache->n_seqs);
+  if (max_prefix_len < 0 || max_prefix_len > cache->capacity)
+    return fail(TQ_ERR_INVALID, "max_prefix_len=%d outside [0, capacity=%d]", max_prefix_len, cache->capacity);
+  if (max_suffix_len < 0 || max_suffix_len > cache->capacity)
+    return fail(TQ_ERR_INVALID, "max_suffix_len=%d outside [0, capacity=%d]", max_suffix_len, cache->capacity);
+  return TQ_OK;
+}
+
+tq::SharedPlan shared_plan(const tq_ctx *ctx, const tq_cache *cache, int32_t n_q_heads, int32_t n_groups,
+                           int32_t max_group, int32_t max_prefix_len, int32_t max_suffix_len) {
+  return tq::plan_shared(ctx->d, ctx->bits_k, ctx->bits_v, ctx->qjl, cache->n_seqs, n_q_heads, cache->n_kv_heads,
+                         n_groups, max_group, max_prefix_len, max_suffix_len);
+}
+
+}  // namespace
+
+size_t tq_shared_workspace_bytes(const tq_ctx *ctx, const tq_cache *cache, int32_t n_q_heads, int32_t n_groups,
+                                 int32_t max_group, int32_t max_prefix_len, int32_t max_suffix_len) {
+  if (!ctx || check_geometry(cache) != TQ_OK || tq::check_context_device(ctx) != TQ_OK ||
+      check_shared_sizes(cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len) != TQ_OK)
+    return 0;
+  return shared_plan(ctx, cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len).workspace;
+}
+
+tq_status tq_decode_attention_shared(tq_ctx *ctx, const tq_cache *cache, const void *q, int32_t q_dtype,
+                                     int32_t n_q_heads, const int32_t *seq_lens, const int32_t *cu_group,
+                                     const int32_t *prefix_lens, int32_t n_groups, int32_t max_group,
+                                     int32_t max_prefix_len, int32_t max_suffix_len, float scale, void *out,
+                                     int32_t out_dtype, float *lse, void *workspace, size_t workspace_bytes,
+                                     void *stream) {
+  if (!ctx) return fail(TQ_ERR_INVALID, "ctx is NULL");
+  tq_status st = tq::check_context_device(ctx);
+  if (st != TQ_OK) return st;
+  st = check_cache(ctx, cache);
+  if (st != TQ_OK) return st;
+  if (!q || !seq_lens || !cu_group || !prefix_lens || !out || !workspace)
+    return fail(TQ_ERR_INVALID, "q, seq_lens, cu_group, prefix_lens, out and workspace must be non-NULL");
+  if (q_dtype != TQ_BF16 && q_dtype != TQ_F32) return fail(TQ_ERR_INVALID, "q_dtype=%d", q_dtype);
+  if (out_dtype != TQ_BF16 && out_dtype != TQ_F32) return fail(TQ_ERR_INVALID, "out_dtype=%d", out_dtype);
+  st = check_shared_sizes(cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len);
+  if (st != TQ_OK) return st;
+  if (!aligned16(q) || !aligned16(out) || ((uintptr_t)workspace & 255u) || ((uintptr_t)seq_lens & 3u) ||
+      ((uintptr_t)cu_group & 3u) || ((uintptr_t)prefix_lens & 3u) || (lse && ((uintptr_t)lse & 3u)))
+    return fail(TQ_ERR_INVALID, "misaligned q/out (16 B), workspace (256 B) or seq_lens/cu_group/prefix_lens/lse (4 B)");
+  if (!std::isfinite(scale)) return fail(TQ_ERR_INVALID, "scale is not finite");
+  const tq::SharedPlan plan =
+      shared_plan(ctx, cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len);
+  if (workspace_bytes < plan.workspace)
+    return fail(TQ_ERR_INVALID, "workspace_bytes=%zu < required %zu", workspace_bytes, plan.workspace);
+  if (scale <= 0.f) scale = 1.0f / std::sqrt((float)ctx->d);
+  const int e = tq::launch_shared(ctx->dp, *cache, q, q_dtype, n_q_heads, seq_lens, cu_group, prefix_lens, n_groups,
+                                  max_group, max_prefix_len, max_suffix_len, scale, out, out_dtype == TQ_F32, lse,
+                                  (char *)workspace, plan, stream);
+  if (e != 0) return cuda_fail((cudaError_t)e, "tq_decode_attention_shared launch");
   return TQ_OK;
 }
 

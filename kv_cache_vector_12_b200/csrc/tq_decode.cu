@@ -5,76 +5,10 @@
 #include <cmath>
 
 #include "tq_decode_kernel.cuh"
+#include "tq_merge.cuh"
 
 namespace tq {
 namespace {
-
-// ---------------------------------------------------------------------------
-// merge: per (sequence, query head) combine the splits (log-sum-exp in log2
-// units) and apply Pi^T.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ float block_max128(float v, float *red) {
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const float r = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  __syncthreads();
-  return r;
-}
-
-// A bf16 row of DH entries (16-byte aligned): held in registers as
-// independent 16-byte loads (DH <= 128, loaded ahead of use) or read on the
-// fly (DH = 256).
-template <int DH>
-struct Bf16Row {
-  static constexpr int kHeld = DH <= 128 ? DH / 8 : 1;
-  uint4 w[kHeld];
-  const uint16_t *row;
-  __device__ __forceinline__ void load(const uint16_t *r) {
-    row = r;
-    if constexpr (DH <= 128) {
-#pragma unroll
-      for (int c = 0; c < DH / 8; ++c) w[c] = reinterpret_cast<const uint4 *>(r)[c];
-    }
-  }
-  __device__ __forceinline__ uint4 get(int c) const {
-    if constexpr (DH <= 128) return w[c];
-    else return reinterpret_cast<const uint4 *>(row)[c];
-  }
-};
-
-// Dot product of a bf16 row with a vector in shared memory, four partial sums.
-template <int DH>
-__device__ __forceinline__ float dot_bf16_row(const Bf16Row<DH> &w, const float *x) {
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int c = 0; c < DH / 8; ++c) {
-    const uint4 v = w.get(c);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = 8 * c + 2 * e;
-      acc[e] = fmaf(__uint_as_float(u[e] << 16), x[j], acc[e]);
-      acc[e] = fmaf(__uint_as_float(u[e] & 0xffff0000u), x[j + 1], acc[e]);
-    }
-  }
-  return (acc[0] + acc[1]) + (acc[2] + acc[3]);
-}
-
-// PL consecutive floats (PL * 4-byte aligned) as vector loads.
-template <int PL>
-__device__ __forceinline__ void load_floats(const float *src, float (&v)[PL]) {
-  if constexpr (PL == 2) {
-    const float2 x = *reinterpret_cast<const float2 *>(src);
-    v[0] = x.x, v[1] = x.y;
-  } else {
-#pragma unroll
-    for (int c = 0; c < PL / 4; ++c) {
-      const float4 x = reinterpret_cast<const float4 *>(src)[c];
-      v[4 * c] = x.x, v[4 * c + 1] = x.y, v[4 * c + 2] = x.z, v[4 * c + 3] = x.w;
-    }
-  }
-}
 
 // ---------------------------------------------------------------------------
 // merge: per (sequence, query head) combine the splits (log-sum-exp in log2
@@ -183,6 +117,13 @@ __global__ void __launch_bounds__(128) merge_kernel(DeviceParams p, int n_q_head
 
 template <int DH>
 DecodeVariant variant_d(int bk, int bv, bool qjl, int nt, int build) {
+  if (build == kShared) {
+    switch (bk) {
+      case 2: return shared_variant<DH, 2>(bv, qjl, nt);
+      case 3: return shared_variant<DH, 3>(bv, qjl, nt);
+      default: return shared_variant<DH, 4>(bv, qjl, nt);
+    }
+  }
   switch (bk) {
     case 2: return decode_variant<DH, 2>(bv, qjl, nt, build);
     case 3: return decode_variant<DH, 3>(bv, qjl, nt, build);
@@ -200,14 +141,10 @@ int build_of(bool long_splits, bool paged) { return paged ? kPaged : long_splits
 
 int dim_index(int d) { return d == 64 ? 0 : d == 128 ? 1 : 2; }
 
-}  // namespace
-
-int decode_ctas_per_sm(int d, int bits_k, int bits_v, int qjl, int group, bool long_splits, bool paged) {
+int ctas_of(int d, int bits_k, int bits_v, int qjl, int nt, int build) {
   // cached per variant; atomically, as calls may come from several threads
   // (per device: the attribute and the occupancy query apply to the current one)
-  static std::atomic<int> cache[kMaxDevices][3][3][3][2][2][3];
-  const int nt = group > 8 ? 2 : 1;
-  const int build = build_of(long_splits, paged);
+  static std::atomic<int> cache[kMaxDevices][3][3][3][2][2][4];
   std::atomic<int> &slot =
       cache[current_device()][dim_index(d)][bits_k - 2][bits_v - 2][qjl ? 1 : 0][nt - 1][build];
   int c = slot.load(std::memory_order_relaxed);
@@ -221,6 +158,20 @@ int decode_ctas_per_sm(int d, int bits_k, int bits_v, int qjl, int group, bool l
     slot.store(c, std::memory_order_relaxed);
   }
   return c;
+}
+
+}  // namespace
+
+int decode_ctas_per_sm(int d, int bits_k, int bits_v, int qjl, int group, bool long_splits, bool paged) {
+  return ctas_of(d, bits_k, bits_v, qjl, group > 8 ? 2 : 1, build_of(long_splits, paged));
+}
+
+int shared_ctas_per_sm(int d, int bits_k, int bits_v, int qjl, int nt) {
+  return ctas_of(d, bits_k, bits_v, qjl, nt, kShared);
+}
+
+DecodeVariant shared_kernel(const DeviceParams &p, int nt) {
+  return variant(p.d, p.bits_k, p.bits_v, p.qjl != 0, nt, kShared);
 }
 
 int launch_decode(const DeviceParams &p, const tq_cache &c, const void *q, int q_dtype, int n_q_heads,

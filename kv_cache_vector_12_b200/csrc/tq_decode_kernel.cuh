@@ -44,6 +44,7 @@
 
 #include "tq_f32x2.cuh"
 #include "tq_internal.h"
+#include "tq_groups.cuh"
 #include "tq_stream.cuh"
 
 namespace tq {
@@ -57,7 +58,17 @@ struct DecodeArgs {
   int q_dtype;
   float scale;
   float *partials;        // [rows][n_splits][d + 4]
+  // groups of sequences that share a prefix (the SHARED build only): this
+  // launch takes either the prefixes, each once for up to `members` of its
+  // group's sequences, or the positions behind them, sequence by sequence
+  const int32_t *cu_group, *prefix;  // [n_groups + 1], [n_groups]
+  int n_groups, max_group, max_prefix, max_suffix;
+  int pass;                          // kPassPrefix or kPassSuffix
+  int members;                       // sequences per CTA of the prefix pass
+  int slot0;                         // first partial slot of this pass (n_splits counts both passes' slots)
 };
+
+enum SharedPass { kPassPrefix = 0, kPassSuffix = 1 };
 
 using DecodeFn = void (*)(const DecodeArgs);
 
@@ -71,12 +82,19 @@ struct DecodeVariant {
 // budget (its callers decode batches of many sequences).  At d = 256 every
 // build runs the 168-register budget (twice the value accumulators), at
 // d = 64 the 128-register one; kShort and kLong are then the same kernel.
-enum Build { kShort = 0, kLong = 1, kPaged = 2 };
+// kShared: the budget of kPaged, either layout, for batches whose groups share
+// a prefix.
+enum Build { kShort = 0, kLong = 1, kPaged = 2, kShared = 3 };
 
 // The instantiations for head dimension DH and K width BK (defined in
 // tq_decode_variants.cu, one object per pair).
 template <int DH, int BK>
 DecodeVariant decode_variant(int bits_v, bool qjl, int nt, int build);
+// The same for the build kShared (tq_shared_variants.cu).
+template <int DH, int BK>
+DecodeVariant shared_variant(int bits_v, bool qjl, int nt);
+// The kShared kernel of a context with 8 nt rows per CTA (tq_decode.cu).
+DecodeVariant shared_kernel(const DeviceParams &p, int nt);
 
 namespace {
 
@@ -177,7 +195,13 @@ __device__ __forceinline__ void qjl_pick(int s, int slot, int q, int &wd, int &j
 // PAGED selects the paged cache layout (the stage copies follow the block
 // table); it is its own instantiation so that the contiguous kernels keep
 // their code and register allocation.
-template <int BK, int BV, bool QJL, int NT, int CTAS, bool PAGED, int DH>
+//
+// SHARED selects the build for groups of sequences that share a prefix
+// (tq_shared.cu): the unit of a CTA is then either some members of a group
+// against the group's prefix, read from its first sequence, or one sequence
+// against the positions behind its prefix.  Its rows are (member, query head)
+// pairs, it takes either layout, and positions below a given one are masked.
+template <int BK, int BV, bool QJL, int NT, int CTAS, bool PAGED, int DH, bool SHARED = false>
 __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const DecodeArgs a) {
   static_assert(kStageTokens % 64 == 0 && kWarpTokens == 32, "stages start on 64-token boundaries");
   static_assert(DH == 64 || DH == 128 || DH == 256, "head dimension");
@@ -201,10 +225,13 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
   __shared__ float s_qs[kRows][4];                                // score factor, QJL factor, sum of q_tilde ints
   __shared__ float s_red[kConsumerWarps][kRows];
 
-  const int split = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
+  const int split = blockIdx.x, h = blockIdx.y;
+  int s = blockIdx.z;  // the sequence whose planes are read
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, q = lane & 3;
-  const int G = a.n_q_heads / a.c.n_kv_heads;
+  const int per = a.n_q_heads / a.c.n_kv_heads;  // query heads per KV head
+  int G = per;                                   // rows of this CTA
+  int first_member = s;                          // SHARED: the sequence of the first row
   // B fragments of Pi (rows in the K fragment order) for this consumer warp's
   // DH / 4 output positions: parameters, loaded before waiting for the
   // previous kernel in the stream (DH = 256: read during the rotation)
@@ -233,7 +260,7 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
   // one more memory round trip, amortised over a long split) and bounds the
   // prefetch by it, so that splits past their sequence's end fetch nothing; a
   // stale value costs at most a useless or a missing prefetch.
-  if (warp == kConsumerWarps && lane == 0) {
+  if (!SHARED && warp == kConsumerWarps && lane == 0) {
     // this KV head's query rows (read right after the wait)
     const size_t qbytes = (size_t)G * DH * (a.q_dtype == TQ_F32 ? 4 : 2);
     prefetch_l2(static_cast<const char *>(a.q) + ((size_t)s * a.n_q_heads + (size_t)h * G) * DH *
@@ -275,6 +302,30 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
   // launched as a programmatic dependent: the cache, q and seq_lens are final
   // once the previous kernel in the stream has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  int t_first = 0, t_low = 0, t_end = 0;  // SHARED: first position copied, first attended, end
+  if constexpr (SHARED) {
+    SharedUnit u;
+    if (a.pass == kPassPrefix) {
+      u = find_members(a.cu_group, a.n_groups, a.max_group, a.members, a.c.n_seqs, blockIdx.z, lane);
+      if (u.count == 0) return;
+      const int len = a.prefix[u.group];
+      // (a prefix outside its bounds is flagged by the other pass)
+      if (len <= 0 || len > a.max_prefix || len > a.c.capacity) return;
+      s = u.lead;
+      first_member = u.first;
+      G = u.count * per;
+      t_end = len;
+    } else {
+      const SeqRange g = sequence_range(a.cu_group, a.prefix, a.n_groups, a.seq_lens, a.max_group, a.max_prefix,
+                                        a.max_suffix, a.c.capacity, s, lane);
+      if (g.bad && tid == 0 && split == 0 && h == 0) atomicOr(a.p.err, kErrSeqLen);
+      if (g.len <= g.prefix) return;
+      t_low = g.prefix;
+      t_first = g.prefix & ~63;  // copies start on 64-token boundaries
+      t_end = g.len;
+    }
+    if (t_first + split * a.chunk >= t_end) return;
+  }
   // the consumers' loads of this KV head's G query rows (contiguous, 16-byte
   // aligned) go out first, beside the length's: they do not depend on it
   constexpr int kQIt = (kRows * DH / 4 + 32 * kConsumerWarps - 1) / (32 * kConsumerWarps);
@@ -282,26 +333,34 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
   const bool q_f32 = a.q_dtype == TQ_F32;
   uint4 q_v[kQIt];  // raw: four fp32, or four bf16 in .x, .y (converted when stored)
   if (warp < kConsumerWarps) {
-    const long q_off = ((long)s * a.n_q_heads + (long)h * G) * DH;
+    const long q_off = ((long)(SHARED ? first_member : s) * a.n_q_heads + (long)h * per) * DH;
 #pragma unroll
     for (int k = 0; k < kQIt; ++k) {
       const int i = tid + 32 * kConsumerWarps * k;
       if (i < q_n4) {
+        // SHARED: the rows of the next member are n_q_heads rows on
+        long at = i;
+        if constexpr (SHARED) at += (long)(i / (per * (DH / 4))) * (a.n_q_heads - per) * (DH / 4);
         if (q_f32) {
-          q_v[k] = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q) + q_off)[i];
+          q_v[k] = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q) + q_off)[at];
         } else {
-          const uint2 u = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + q_off)[i];
+          const uint2 u = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + q_off)[at];
           q_v[k] = make_uint4(u.x, u.y, 0u, 0u);
         }
       }
     }
   }
-  int len = a.seq_lens[s];
-  if (len < 0 || len > a.max_seq_len) {
-    if (tid == 0 && split == 0 && h == 0) atomicOr(a.p.err, kErrSeqLen);
-    len = len < 0 ? 0 : a.max_seq_len;
+  int len;
+  if constexpr (SHARED) {
+    len = t_end;
+  } else {
+    len = a.seq_lens[s];
+    if (len < 0 || len > a.max_seq_len) {
+      if (tid == 0 && split == 0 && h == 0) atomicOr(a.p.err, kErrSeqLen);
+      len = len < 0 ? 0 : a.max_seq_len;
+    }
   }
-  const int t0 = split * a.chunk;
+  const int t0 = t_first + split * a.chunk;
   if (t0 >= len) return;  // this split holds no tokens; merge skips it
   const int t1 = min(len, t0 + a.chunk);
   const int n_stage = (t1 - t0 + kStageTokens - 1) / kStageTokens;
@@ -329,7 +388,7 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
         const uint32_t n = (uint32_t)min(kStageTokens, (t1 - first + 63) & ~63);
         const uint32_t bytes = n * (D * BK / 8 + D * BV / 8 + 4 + (QJL ? D / 8 + 2 : 0));
         mbar_arrive_expect_tx(bar, bytes);
-        if constexpr (!PAGED) {
+        if (!PAGED || (SHARED && !a.c.block_table)) {
           const long tok = base + first;
           bulk_g2s(smem_u32(st + St::kc), a.c.codes_k + tok * (D * BK / 8), n * (D * BK / 8), bar);
           bulk_g2s(smem_u32(st + St::vc), a.c.codes_v + tok * (D * BV / 8), n * (D * BV / 8), bar);
@@ -382,7 +441,6 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
     // hi + lo pair so every product is exact and the sums are fp32.  Warp w
     // computes positions (D / 4) w .. (D / 4) w + D / 4 - 1.
     {
-      const long qrow0 = (long)s * a.n_q_heads + (long)h * G;
       const bool f32 = a.q_dtype == TQ_F32;
       // the G query rows, loaded right after the dependency wait, into
       // shared memory
@@ -698,7 +756,8 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
         const __half *kn = reinterpret_cast<const __half *>(st + St::kn) + wt;
         const __half *vn = reinterpret_cast<const __half *>(st + St::vn) + wt;
         float nk[4], nv[4], gm[4];
-        const bool partial = tok0 + kWarpTokens > t1;  // only the last tile of a split is ragged
+        // only the last tile of a split is ragged (SHARED: the first of the suffix too)
+        const bool partial = tok0 + kWarpTokens > t1 || (SHARED && tok0 < t_low);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int tt = 16 * (u >> 1) + r + 8 * (u & 1);
@@ -706,7 +765,7 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
           nv[u] = __half2float(vn[tt]);
           gm[u] = 0.f;
           if constexpr (QJL) gm[u] = __half2float(reinterpret_cast<const __half *>(st + St::jg)[wt + tt]);
-          if (partial && tok0 + tt >= t1) nk[u] = nv[u] = gm[u] = __int_as_float(0x7fc00000);  // NaN marks "masked"
+          if (partial && (tok0 + tt >= t1 || (SHARED && tok0 + tt < t_low))) nk[u] = nv[u] = gm[u] = __int_as_float(0x7fc00000);  // NaN marks "masked"
         }
         uint32_t pb[2][NT][2];
         bool rescale = false;
@@ -1042,7 +1101,10 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
       l = fmaf(f, sm_l[w][g], l);
       o = fmaf(f, so[(w * 8 * NT + g) * D + i], o);
     }
-    float *dst = a.partials + (((long)s * a.n_q_heads + h * G + g) * a.n_splits + split) * (D + 4);
+    long out_row;
+    if constexpr (SHARED) out_row = (long)(first_member + g / per) * a.n_q_heads + h * per + g % per;
+    else out_row = (long)s * a.n_q_heads + h * G + g;
+    float *dst = a.partials + (out_row * a.n_splits + (SHARED ? a.slot0 : 0) + split) * (D + 4);
     dst[4 + i] = o;
     if (i == 0) {
       dst[0] = mx;
@@ -1061,10 +1123,12 @@ constexpr int decode_smem_bytes() {
 
 
 
-template <int BK, int BV, bool QJL, int NT, int DH>
+template <int BK, int BV, bool QJL, int NT, int DH, bool SHARED>
 DecodeVariant variant_c(int build) {
   constexpr int smem = decode_smem_bytes<BK, BV, QJL, NT, DH>();
-  if constexpr (DH == 128) {
+  if constexpr (SHARED) {
+    return {decode_mma_kernel<BK, BV, QJL, NT, DH == 256 ? 2 : 3, true, DH, true>, smem};
+  } else if constexpr (DH == 128) {
     if (build == kPaged) return {decode_mma_kernel<BK, BV, QJL, NT, 3, true, DH>, smem};
     if (build == kLong) return {decode_mma_kernel<BK, BV, QJL, NT, 3, false, DH>, smem};
     return {decode_mma_kernel<BK, BV, QJL, NT, 2, false, DH>, smem};
@@ -1075,22 +1139,22 @@ DecodeVariant variant_c(int build) {
   }
 }
 
-template <int BK, int BV, bool QJL, int DH>
+template <int BK, int BV, bool QJL, int DH, bool SHARED>
 DecodeVariant variant_q(int nt, int build) {
-  return nt == 1 ? variant_c<BK, BV, QJL, 1, DH>(build) : variant_c<BK, BV, QJL, 2, DH>(build);
+  return nt == 1 ? variant_c<BK, BV, QJL, 1, DH, SHARED>(build) : variant_c<BK, BV, QJL, 2, DH, SHARED>(build);
 }
 
-template <int BK, int BV, int DH>
+template <int BK, int BV, int DH, bool SHARED>
 DecodeVariant variant_v(bool qjl, int nt, int build) {
-  return qjl ? variant_q<BK, BV, true, DH>(nt, build) : variant_q<BK, BV, false, DH>(nt, build);
+  return qjl ? variant_q<BK, BV, true, DH, SHARED>(nt, build) : variant_q<BK, BV, false, DH, SHARED>(nt, build);
 }
 
-template <int BK, int DH>
+template <int BK, int DH, bool SHARED = false>
 DecodeVariant variant_k(int bv, bool qjl, int nt, int build) {
   switch (bv) {
-    case 2: return variant_v<BK, 2, DH>(qjl, nt, build);
-    case 3: return variant_v<BK, 3, DH>(qjl, nt, build);
-    default: return variant_v<BK, 4, DH>(qjl, nt, build);
+    case 2: return variant_v<BK, 2, DH, SHARED>(qjl, nt, build);
+    case 3: return variant_v<BK, 3, DH, SHARED>(qjl, nt, build);
+    default: return variant_v<BK, 4, DH, SHARED>(qjl, nt, build);
   }
 }
 

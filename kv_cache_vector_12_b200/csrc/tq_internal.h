@@ -87,6 +87,8 @@ DecodeSplit decode_split(int n_seqs, int n_kv_heads, int max_seq_len, int ctas_p
 // KV head, with the long-split (128-register) or short-split (168) budget, or
 // the paged-layout build (128 registers).
 int decode_ctas_per_sm(int d, int bits_k, int bits_v, int qjl, int group, bool long_splits, bool paged);
+// The same for the build for groups that share a prefix, 8 nt rows per CTA.
+int shared_ctas_per_sm(int d, int bits_k, int bits_v, int qjl, int nt);
 // The split and register budget of one decode call (tq_api.cu).
 DecodeSplit plan_decode(int d, int bits_k, int bits_v, int qjl, int group, int n_seqs, int n_kv_heads,
                         int max_seq_len, bool paged);
@@ -168,6 +170,21 @@ int launch_tables(const DeviceParams &p, const tq_cache &c, int32_t *block_table
                   const int32_t *fresh, const int32_t *free_list, int n_free, const int32_t *free_start,
                   int32_t *free_end, const int32_t *cu_group, const int32_t *prefix, int n_groups, int n_tok,
                   int32_t *seq_idx, int32_t *pos, int64_t *slots, int32_t *cu_new, int32_t *seq_lens, void *stream);
+// Decode attention for groups of sequences that share a prefix (tq_shared.cu):
+// how the two passes cut their units, and the launch.
+struct SharedPlan {
+  int nt_p, members, units;  // prefix pass: 8 nt_p rows, up to `members` sequences per CTA, units over all groups
+  int p_chunk, p_splits;     // its split of [0, prefix) (p_splits = 0: no prefix)
+  int nt_s;                  // pass behind the prefix: one sequence per CTA
+  int s_chunk, s_splits;     // its split of [prefix rounded down to 64, len)
+  size_t workspace;          // partials [n_seqs n_q_heads][p_splits + s_splits][d + 4]
+};
+SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n_q_heads, int n_kv_heads, int n_groups,
+                       int max_group, int max_prefix, int max_suffix);
+int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q_dtype, int n_q_heads,
+                  const int32_t *seq_lens, const int32_t *cu_group, const int32_t *prefix, int n_groups,
+                  int max_group, int max_prefix, int max_suffix, float scale, void *out, bool out_f32, float *lse,
+                  char *workspace, const SharedPlan &plan, void *stream);
 int launch_decode(const DeviceParams &p, const tq_cache &c, const void *q, int q_dtype,
                   int n_q_heads, const int32_t *seq_lens, int max_seq_len, float scale,
                   float *out, float *lse, char *workspace, const DecodeSplit &split,

@@ -69,6 +69,11 @@ lib.tq_weight_workspace_bytes.restype = ctypes.c_size_t
 lib.tq_weight_gemm.argtypes = [_vp, ctypes.POINTER(tq_cache), _i32, _i32, _vp, _i32, _i32, _vp, _vp,
                                ctypes.c_size_t, _vp]
 lib.tq_weight_gemm.restype = ctypes.c_int
+lib.tq_shared_workspace_bytes.argtypes = [_vp, ctypes.POINTER(tq_cache), _i32, _i32, _i32, _i32, _i32]
+lib.tq_shared_workspace_bytes.restype = ctypes.c_size_t
+lib.tq_decode_attention_shared.argtypes = [_vp, ctypes.POINTER(tq_cache), _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32,
+                                           _i32, _i32, ctypes.c_float, _vp, _i32, _vp, _vp, ctypes.c_size_t, _vp]
+lib.tq_decode_attention_shared.restype = ctypes.c_int
 lib.tq_prompt_attention.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _i32, _i32, _i32,
                                     _vp, _i32, _i32, ctypes.c_float, _vp, _i32, _vp, _vp]
 lib.tq_prompt_attention.restype = ctypes.c_int
@@ -279,6 +284,29 @@ def decode_attention_noalloc(ctx: Context, cache: Cache, q: torch.Tensor, seq_le
                                            _stream(stream)))
 
 
+def shared_workspace_bytes(ctx: Context, cache: Cache, n_q_heads: int, n_groups: int, max_group: int,
+                           max_prefix_len: int, max_suffix_len: int) -> int:
+    return int(lib.tq_shared_workspace_bytes(ctx.handle, ctypes.byref(cache.struct), n_q_heads, n_groups, max_group,
+                                             max_prefix_len, max_suffix_len))
+
+
+def decode_attention_shared(ctx: Context, cache: Cache, q: torch.Tensor, seq_lens: torch.Tensor,
+                            cu_group: torch.Tensor, prefix_lens: torch.Tensor, max_group: int, max_prefix_len: int,
+                            max_suffix_len: int, out: torch.Tensor, lse: torch.Tensor | None,
+                            workspace: torch.Tensor, scale: float = 0.0, stream=None) -> None:
+    """tq_decode_attention_shared: decode attention for groups of sequences
+    (cu_group int32 [n_groups + 1]) that share their first prefix_lens[g]
+    (int32 [n_groups]) positions, read from the group's first sequence; q
+    [n_seqs, n_q_heads, d] bf16 or fp32, out bf16 or fp32 of the same shape."""
+    q_dtype = TQ_F32 if q.dtype == torch.float32 else TQ_BF16
+    out_dtype = TQ_F32 if out.dtype == torch.float32 else TQ_BF16
+    _check(lib.tq_decode_attention_shared(ctx.handle, ctypes.byref(cache.struct), _ptr(q), q_dtype, q.shape[1],
+                                          _ptr(seq_lens), _ptr(cu_group), _ptr(prefix_lens), prefix_lens.numel(),
+                                          max_group, max_prefix_len, max_suffix_len, scale, _ptr(out), out_dtype,
+                                          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                          _stream(stream)))
+
+
 def prompt_attention(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
                      max_len: int, out: torch.Tensor, lse: torch.Tensor | None = None, scale: float = 0.0,
                      stream=None) -> None:
@@ -352,4 +380,10 @@ def weight_gemm(ctx: Context, wc: WeightCache, x: torch.Tensor, y: torch.Tensor,
 
 def alloc_workspace(ctx: Context, n_seqs: int, n_q_heads: int, max_seq_len: int, device="cuda") -> torch.Tensor:
     n = workspace_bytes(ctx, n_seqs, n_q_heads, max_seq_len)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def alloc_shared_workspace(ctx: Context, cache: Cache, n_q_heads: int, n_groups: int, max_group: int,
+                           max_prefix_len: int, max_suffix_len: int, device="cuda") -> torch.Tensor:
+    n = shared_workspace_bytes(ctx, cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)

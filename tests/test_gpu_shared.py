@@ -1,0 +1,354 @@
+"""Decode attention for groups that share a prefix (tq_decode_attention_shared)
+against the definition in 64 bits on the same packed bytes: the group's first
+sequence holds positions below the prefix, each member the ones behind it.
+
+The bound is the library's for attention over the packed cache, 1e-3 of a
+row's largest output (and of the largest score for the lse): the softmax
+weights times the value norms are rounded to fp16 (2^-11) and q to 16 bits,
+all else is fp32; a bf16 output adds its own half step, 2^-8 of the value."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import turboquant_oracle as o
+from tests import parity_helpers as ph
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tq(cuda_device):
+    from kv_cache_vector_12_b200 import tq as tqmod
+    return tqmod
+
+
+_params = {}
+
+
+def params(d, bits_k, bits_v, qjl):
+    key = (d, bits_k, bits_v, qjl)
+    if key not in _params:
+        _params[key] = o.Params(d, bits_k, bits_v, bool(qjl), 42)
+    return _params[key]
+
+
+class Batch:
+    """A packed cache of random bytes and norms; what no call may use is NaN
+    norms (all 16 bits of the norm planes set)."""
+
+    def __init__(self, tq, groups, prefixes, lens, n_kv=2, per=4, d=128, bits_k=3, bits_v=3, qjl=0, block=0, seed=0,
+                 q_dtype=torch.float32, norm=11.0):
+        self.tq, self.groups, self.prefixes, self.lens = tq, groups, prefixes, lens
+        self.n_kv, self.per, self.d, self.block = n_kv, per, d, block
+        self.bits_k, self.bits_v, self.qjl = bits_k, bits_v, qjl
+        self.ctx = tq.Context(d, bits_k, bits_v, qjl, 42)
+        n = len(lens)
+        rng = np.random.default_rng(seed)
+        self.group_of = [next((g for g in range(len(prefixes)) if groups[g] <= s < groups[g + 1]), None)
+                         for s in range(n)]
+        unit = block or 64
+        longest = max([1] + list(lens) + list(prefixes))
+        self.cap = -(-longest // unit) * unit + unit
+        # (sequence, position) -> row of the planes
+        if block:
+            per_seq = self.cap // block
+            table, used = np.full((n, per_seq), -1, dtype=np.int32), 0
+            for s in range(n):
+                g = self.group_of[s]
+                lead = s if g is None else groups[g]
+                p = 0 if g is None else prefixes[g]
+                upto = max(lens[s], p) if s == lead else lens[s]
+                # a member's table holds its own blocks from the prefix's end on (whole shared blocks: anything)
+                first = 0 if s == lead else p // block
+                for j in range(first, -(-upto // block)):
+                    table[s, j] = used
+                    used += 1
+            perm = rng.permutation(used + 3)
+            table = np.where(table >= 0, perm[table], table).astype(np.int32)
+            self.cache = tq.PagedCache(self.ctx, n, n_kv, self.cap, block, n_blocks=used + 3,
+                                       block_table=torch.from_numpy(table))
+            self.table = table
+        else:
+            self.cache = tq.Cache(self.ctx, n, n_kv, self.cap)
+        self.planes = {}
+        for name, t in self.cache.planes.items():
+            if t is None:
+                continue
+            if t.dtype == torch.uint8:
+                a = rng.integers(0, 256, t.shape, dtype=np.uint8)
+            else:
+                x = {"norm_k": norm, "norm_v": 1.0, "qjl_norm": 0.2}[name] * np.exp(0.3 * rng.standard_normal(t.shape))
+                a = x.astype(np.float16).view(np.int16)
+                a = self._poison(a)
+            self.planes[name] = a
+            t.copy_(torch.from_numpy(a))
+        self.q = torch.from_numpy(rng.standard_normal((n, n_kv * per, d)).astype(np.float32)).to(q_dtype).cuda()
+
+    def _slot(self, s, p):
+        if self.block:
+            return self.table[s, p // self.block], p % self.block
+        return s, p
+
+    def _poison(self, a):
+        """NaN wherever no position of the definition lies."""
+        used = np.zeros((a.shape[0], a.shape[2]), dtype=bool)
+        for s, n in enumerate(self.lens):
+            g = self.group_of[s]
+            p = 0 if g is None else self.prefixes[g]
+            lead = s if g is None else self.groups[g]
+            for x, seq in ((np.arange(p), lead), (np.arange(p, n), s)):
+                if len(x):
+                    if self.block:
+                        used[self.table[seq, x // self.block], x % self.block] = True
+                    else:
+                        used[seq, x] = True
+        for g, p in enumerate(self.prefixes):  # an inactive first sequence holds the prefix too
+            if self.groups[g] < self.groups[g + 1] and p:
+                x, seq = np.arange(p), self.groups[g]
+                if self.block:
+                    used[self.table[seq, x // self.block], x % self.block] = True
+                else:
+                    used[seq, x] = True
+        return np.where(used[:, None, :], a, np.int16(-1))
+
+    def rows(self, name, s, h, a, b):
+        x = np.arange(a, b)
+        if self.block:
+            return self.planes[name][self.table[s, x // self.block], h, x % self.block]
+        return self.planes[name][s, h, x]
+
+    def call(self, out_dtype=torch.float32, scale=0.0, stream=None, max_group=None, max_prefix=None, max_suffix=None,
+             workspace=None, out=None, lse=None):
+        tq, dev = self.tq, "cuda"
+        n = len(self.lens)
+        mg = max_group or max([1] + [b - a for a, b in zip(self.groups, self.groups[1:])])
+        mp = max(self.prefixes) if max_prefix is None else max_prefix
+        suffix = [x - (0 if g is None else self.prefixes[g]) for x, g in zip(self.lens, self.group_of) if x]
+        ms = max([0] + suffix) if max_suffix is None else max_suffix
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+        if workspace is None:
+            workspace = tq.alloc_shared_workspace(self.ctx, self.cache, self.n_kv * self.per, len(self.prefixes), mg, mp, ms)
+            workspace.fill_(0xFF)  # NaN: nothing may be read that was not written
+        if out is None:
+            out = torch.full(self.q.shape, 7.0, dtype=out_dtype, device=dev)
+            lse = torch.full(self.q.shape[:2], 7.0, device=dev)
+        tq.decode_attention_shared(self.ctx, self.cache, self.q, ints(self.lens), ints(self.groups),
+                                   ints(self.prefixes), mg, mp, ms, out, lse, workspace, scale=scale, stream=stream)
+        return out, lse
+
+    def check(self, out, lse, scale=None, skip=(), large=False):
+        p = params(self.d, self.bits_k, self.bits_v, self.qjl)
+        f16 = ph.f16_bits_to_f64
+        bf16 = out.dtype == torch.bfloat16
+        got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        q = self.q.double().cpu().numpy()
+        for s, n in enumerate(self.lens):
+            if s in skip:
+                continue
+            if n == 0:
+                assert (got[s] == 0).all() and (got_lse[s] == -math.inf).all(), s
+                continue
+            g = self.group_of[s]
+            lead, pre = self.groups[g], self.prefixes[g]
+            for h in range(self.n_kv):
+                cat = lambda name: np.concatenate([self.rows(name, lead, h, 0, pre), self.rows(name, s, h, pre, n)])  # noqa: E731
+                heads = slice(h * self.per, (h + 1) * self.per)
+                extra = {}
+                if self.qjl:
+                    extra = dict(s_matrix=p.s, qjl_signs=o.unpack_signs(cat("qjl_bits"), self.d),
+                                 qjl_gamma=f16(cat("qjl_norm")))
+                ref, ref_lse, scores = o.decode_attention(
+                    q[s, heads], p.pi, p.ck, o.unpack_codes(cat("codes_k"), self.bits_k, self.d), f16(cat("norm_k")),
+                    p.cv, o.unpack_codes(cat("codes_v"), self.bits_v, self.d), f16(cat("norm_v")),
+                    scale or 1 / math.sqrt(self.d), **extra)
+                top = np.abs(ref).max(axis=1, keepdims=True)
+                tol = 1e-3 * top + (2.0 ** -8 * np.abs(ref) if bf16 else 0)
+                if large:
+                    # q_hat is held in steps of max|q_hat| / 32767, so a coordinate is off by at most half of one
+                    # and a score by E = scale n_j |half step| sum_i |c_i| <= E_max; every weight is then off by a
+                    # factor within exp(+-2 E_max), and the output by (exp(2 E_max) - 1) sum_j p_j |v_j|
+                    q_hat = q[s, heads] @ p.pi.T
+                    keys = np.abs(np.asarray(p.ck)[o.unpack_codes(cat("codes_k"), self.bits_k, self.d)]).sum(1)
+                    e_max = (np.abs(q_hat).max(1) / 65534 * (f16(cat("norm_k")) * keys).max() / math.sqrt(self.d))[:, None]
+                    w = np.exp(scores - ref_lse[:, None])
+                    vals = (f16(cat("norm_v"))[:, None] * np.asarray(p.cv)[o.unpack_codes(cat("codes_v"), self.bits_v, self.d)]) @ p.pi
+                    tol = tol + np.expm1(2 * e_max) * (w @ np.abs(vals))
+                err = np.abs(got[s, heads] - ref)
+                assert (err <= tol).all(), (s, h, (err / tol).max())
+                big = np.maximum(1.0, np.abs(scores).reshape(self.per, -1).max(axis=1))
+                assert (np.abs(got_lse[s, heads] - ref_lse) <= 1e-3 * big).all(), (s, h)
+
+    def run(self, large=False, **kw):
+        out, lse = self.call(**kw)
+        self.ctx.check_device_errors()
+        self.check(out, lse, kw.get("scale"), large=large)
+
+
+SETTINGS = [(2, 2, 0), (3, 3, 0), (4, 4, 0), (3, 2, 0), (2, 4, 1), (3, 3, 1), (4, 2, 1)]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bits_k,bits_v,qjl", SETTINGS)
+def test_settings_and_head_dimensions(tq, d, bits_k, bits_v, qjl):
+    Batch(tq, [0, 3, 5], [300, 129], [301, 380, 300, 129, 200], d=d, bits_k=bits_k, bits_v=bits_v, qjl=qjl, seed=d).run()
+
+
+@pytest.mark.parametrize("prefix", [0, 1, 63, 64, 65, 127, 128, 1000])
+@pytest.mark.parametrize("suffix", [0, 1, 64, 130])
+def test_prefix_and_suffix_lengths(tq, prefix, suffix):
+    lens = [prefix + suffix, prefix + max(0, suffix - 1), prefix]
+    Batch(tq, [0, 3], [prefix], lens, seed=prefix + suffix).run()
+
+
+@pytest.mark.parametrize("per", [1, 2, 3, 5, 7, 8, 11, 16])
+@pytest.mark.parametrize("n", [1, 2, 6, 19])
+def test_group_sizes_and_query_heads(tq, per, n):
+    rng = np.random.default_rng(per * n)
+    lens = (200 + rng.integers(0, 90, n)).tolist()
+    Batch(tq, [0, n], [200], lens, n_kv=2, per=per, seed=n).run()
+
+
+@pytest.mark.parametrize("per,n", [(4, 33), (8, 16), (8, 17), (7, 37), (16, 9), (1, 130), (3, 90)])
+def test_large_groups(tq, per, n):
+    """More rows than one matrix tile of 128 holds, and just as many."""
+    rng = np.random.default_rng(per * n)
+    lens = (500 + rng.integers(0, 40, n)).tolist()
+    Batch(tq, [0, n], [500], lens, n_kv=1, per=per, seed=n, q_dtype=torch.bfloat16).run()
+
+
+@pytest.mark.parametrize("block", [64, 128, 256])
+@pytest.mark.parametrize("qjl", [0, 1])
+def test_paged_members_tables_hold_only_their_own_blocks(tq, block, qjl):
+    """Unequal groups, one of them empty, one of one sequence; sequences that take no part, the first of a group too."""
+    lens = [700, 612, 0, 612, 0, 335, 333, 512, 50, 0, 0]
+    Batch(tq, [0, 4, 4, 7, 8, 11], [612, 100, 333, 512, 0], lens, block=block, qjl=qjl, seed=block).run()
+
+
+def test_bf16_output_and_given_scale(tq):
+    b = Batch(tq, [0, 5], [900], [901, 950, 900, 1030, 1000], q_dtype=torch.bfloat16)
+    b.run(out_dtype=torch.bfloat16)
+    b.run(out_dtype=torch.bfloat16, scale=0.5)
+
+
+def test_large_norms(tq):
+    """Scores of some hundreds (key norms of some hundreds, as a model without key normalisation has)."""
+    Batch(tq, [0, 4], [700], [730, 701, 720, 760], norm=400.0, bits_k=4, bits_v=4, seed=1).run(large=True)
+    Batch(tq, [0, 40], [700], [700 + i for i in range(40)], norm=400.0, bits_k=4, bits_v=4, seed=1).run(large=True)
+
+
+@pytest.mark.parametrize("n,per", [(4, 4), (32, 4)])
+def test_long_prefix_over_many_splits(tq, n, per):
+    rng = np.random.default_rng(n)
+    Batch(tq, [0, n], [20001], (20001 + rng.integers(0, 700, n)).tolist(), n_kv=1, per=per, seed=3).run()
+
+
+def test_many_groups(tq):
+    """More groups than a warp holds."""
+    rng = np.random.default_rng(2)
+    sizes = rng.integers(0, 4, 71).tolist()
+    groups = [0] + np.cumsum(sizes).tolist()
+    prefixes = rng.integers(0, 200, 71).tolist()
+    lens = [prefixes[g] + int(rng.integers(0, 80)) for g, k in enumerate(sizes) for _ in range(k)]
+    Batch(tq, groups, prefixes, lens, n_kv=1, per=2, seed=7).run()
+
+
+def test_equals_decode_attention_over_copies(tq):
+    """The same values as tq_decode_attention where every sequence holds the prefix itself."""
+    n, prefix, lens = 3, 640, [700, 641, 777]
+    b = Batch(tq, [0, n], [prefix], lens)
+    out, lse = b.call()
+    for t in b.cache.planes.values():
+        if t is not None:
+            t[1:, :, :prefix] = t[:1, :, :prefix]
+    ref, ref_lse = torch.empty_like(out), torch.empty_like(lse)
+    ws = tq.alloc_workspace(b.ctx, n, out.shape[1], max(lens))
+    tq.decode_attention(b.ctx, b.cache, b.q, torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens), ref,
+                        ref_lse, ws)
+    b.ctx.check_device_errors()
+    assert ((out - ref).abs() <= 1e-3 * ref.abs().amax(-1, keepdim=True)).all()
+
+
+def test_bounds_are_flagged_and_the_others_stay_right(tq):
+    def flagged(b, skip, **kw):
+        out, lse = b.call(**kw)
+        with pytest.raises(tq.TQError) as ei:
+            b.ctx.check_device_errors()
+        assert ei.value.status == tq.TQ_ERR_DEVICE and "seq_len" in str(ei.value)
+        for s in skip:
+            assert (out[s] == 0).all() and (lse[s] == -math.inf).all()
+        b.check(out, lse, skip=skip)
+
+    flagged(Batch(tq, [0, 3], [100], [150, 99, 120]), [1])                          # shorter than the prefix
+    flagged(Batch(tq, [0, 3], [100], [150, 110, 120]), [0], max_suffix=49)          # longer than the bound
+    flagged(Batch(tq, [0, 2, 4], [100, 200], [150, 110, 220, 201]), [2, 3], max_prefix=199)
+    flagged(Batch(tq, [0, 3, 4], [100, 50], [150, 110, 120, 60]), [0, 1, 2], max_group=2)
+    flagged(Batch(tq, [0, 2], [100], [150, 110, 120]), [2])                         # outside every group
+    b = Batch(tq, [0, 2], [100], [150, 110])
+    b.lens = [-5, 110]
+    flagged(b, [0])
+    b.lens = [2 ** 31 - 1, 110]
+    flagged(b, [0], max_suffix=64)
+
+
+def test_captured_replayed_and_on_another_stream(tq):
+    b = Batch(tq, [0, 3, 5], [300, 129], [301, 380, 300, 129, 200])
+    mg, mp, ms = 3, 300, 128
+    ws = tq.alloc_shared_workspace(b.ctx, b.cache, b.n_kv * b.per, 2, mg, mp, ms)
+    first, first_lse = b.call(workspace=ws, max_suffix=ms)
+    torch.cuda.synchronize()
+    out, lse = torch.zeros_like(first), torch.zeros_like(first_lse)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens, groups, prefixes = ints(b.lens), ints(b.groups), ints(b.prefixes)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tq.decode_attention_shared(b.ctx, b.cache, b.q, lens, groups, prefixes, mg, mp, ms, out, lse, ws)
+    ws.fill_(0xFF)
+    graph.replay()
+    b.ctx.check_device_errors()
+    assert torch.equal(out, first) and torch.equal(lse, first_lse)
+    lens.copy_(ints([330, 0, 310, 257, 140]))  # other lengths under the same bounds
+    graph.replay()
+    b.ctx.check_device_errors()
+    side = torch.cuda.Stream()
+    b2 = torch.zeros_like(out), torch.zeros_like(lse)
+    torch.cuda.synchronize()
+    tq.decode_attention_shared(b.ctx, b.cache, b.q, lens, groups, prefixes, mg, mp, ms, *b2, ws, stream=side)
+    side.synchronize()
+    # bit for bit: the longer lengths reach norms that were never written (NaN), which two outputs then share
+    assert torch.equal(out.view(torch.int32), b2[0].view(torch.int32))
+    assert torch.equal(lse.view(torch.int32), b2[1].view(torch.int32)) and not lse[1].isnan().any()
+
+
+def test_refusals(tq):
+    b = Batch(tq, [0, 2], [64], [80, 90])
+    ok = dict(seq_lens=torch.tensor([80, 90], dtype=torch.int32, device="cuda"),
+              cu_group=torch.tensor([0, 2], dtype=torch.int32, device="cuda"),
+              prefix_lens=torch.tensor([64], dtype=torch.int32, device="cuda"), max_group=2, max_prefix_len=64,
+              max_suffix_len=64, out=torch.full(b.q.shape, 7.0, device="cuda"),
+              lse=torch.full(b.q.shape[:2], 7.0, device="cuda"), q=b.q)
+    ws = tq.alloc_shared_workspace(b.ctx, b.cache, 8, 1, 2, 64, 64)
+
+    def refused(status=tq.TQ_ERR_INVALID, workspace=ws, cache=b.cache, **kw):
+        with pytest.raises(tq.TQError) as ei:
+            tq.decode_attention_shared(b.ctx, cache, workspace=workspace, **{**ok, **kw})
+        assert ei.value.status == status
+
+    refused(max_group=0)
+    refused(max_group=3)
+    refused(max_prefix_len=b.cap + 1)
+    refused(max_prefix_len=-1)
+    refused(max_suffix_len=b.cap + 1)
+    refused(seq_lens=None)
+    refused(cu_group=None)
+    refused(scale=float("inf"))
+    refused(q=b.q[:, :7])
+    refused(workspace=ws[:256])
+    refused(workspace=torch.empty(ws.numel() + 16, dtype=torch.uint8, device="cuda")[16:])
+    refused(prefix_lens=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    refused(status=tq.TQ_ERR_UNSUPPORTED, q=torch.zeros(2, 34, 128, device="cuda"))
+    assert tq.shared_workspace_bytes(b.ctx, b.cache, 8, 1, 3, 64, 64) == 0
+    assert tq.shared_workspace_bytes(b.ctx, b.cache, 7, 1, 2, 64, 64) == 0
+    b.ctx.check_device_errors()
+    assert (ok["out"] == 7.0).all()
