@@ -173,6 +173,7 @@ int launch_tables(const DeviceParams &p, const tq_cache &c, int32_t *block_table
 // Decode attention for groups of sequences that share a prefix (tq_shared.cu):
 // how the two passes cut their units, and the launch.
 struct SharedPlan {
+  bool tc;                   // the prefix pass runs on tcgen05, 128 rows per CTA
   int nt_p, members, units;  // prefix pass: 8 nt_p rows, up to `members` sequences per CTA, units over all groups
   int p_chunk, p_splits;     // its split of [0, prefix) (p_splits = 0: no prefix)
   int nt_s;                  // pass behind the prefix: one sequence per CTA

@@ -38,6 +38,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "tq_expand.cuh"
 #include "tq_f32x2.cuh"
 #include "tq_internal.h"
 #include "tq_stream.cuh"
@@ -665,13 +666,10 @@ namespace tq {
 namespace {
 
 constexpr int kTcRows = 128;                      // query rows per CTA
-constexpr int kTcKeys = 128;                      // keys per tile
 constexpr int kTcExpWarp0 = 8;                    // warps 8-11 expand (0-7: softmax)
 constexpr int kTcProdWarp = 12, kTcMmaWarp = 13;
 constexpr int kTcThreads = 32 * 14;
 constexpr int kTcStages = 2;
-constexpr int kOpBytes = 128 * kHeadDim * 2;      // one 128 x 128 16-bit operand: two 128 x 64 swizzled boxes
-constexpr int kOpBox = kOpBytes / 2;
 constexpr uint32_t kTcCols = 512;
 constexpr uint32_t kTcS = 0, kTcO = 128, kTcQ = 256, kTcP = 384;  // tensor-memory columns
 
@@ -690,14 +688,6 @@ struct TcLayout {
 __device__ __forceinline__ void tcx_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tcx_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Byte offset of element (row, col) of a 128 x 128 16-bit operand stored as
-// two boxes of 128 rows x 64 columns, 128-byte rows, 16-byte chunks swizzled
-// by the row within each 8-row (1024-byte) atom.
-__device__ __forceinline__ uint32_t sw_off(int row, int col) {
-  const int box = col >> 6, cc = col & 63;
-  return (uint32_t)(box * kOpBox + row * 128 + ((((cc >> 3) ^ (row & 7)) & 7) << 4) + ((cc & 7) << 1));
-}
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
 // 1024 bytes apart.
@@ -752,124 +742,6 @@ __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
   asm volatile(""
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
-
-// fp16 pairs (codes 0, 1) and (codes 2, 3) of one lookup's low and high bytes.
-__device__ __forceinline__ void f16_pairs(uint32_t lo, uint32_t hi, uint32_t &p01, uint32_t &p23) {
-  p01 = prmt(lo, hi, 0x5140u);
-  p23 = prmt(lo, hi, 0x7362u);
-}
-
-// K~ and V~^T of one tile of keys (ew: the expanding warp 0-3, keys
-// 32 ew .. 32 ew + 31) into the operand buffers kt and vt.
-template <int BK, int BV>
-__device__ __forceinline__ void expand_tile(const unsigned char *st, unsigned char *kt, unsigned char *vt,
-                                            const Lut &lkf, const Lut &lv, int ew, int r, int q) {
-  using St = Stage<BK, BV, false, kTcKeys>;
-#pragma unroll
-  for (int rb = 0; rb < 2; ++rb) {
-    const int k0 = 32 * ew + 16 * rb + r, k1 = k0 + 8;
-    uint32_t wk0[BK], wk1[BK];
-    const unsigned char *kr0 = st + St::kc + k0 * (D * BK / 8) + q * 4 * BK;
-    const unsigned char *kr1 = st + St::kc + k1 * (D * BK / 8) + q * 4 * BK;
-#pragma unroll
-    for (int i = 0; i < BK; ++i) {
-      wk0[i] = reinterpret_cast<const uint32_t *>(kr0)[i];
-      wk1[i] = reinterpret_cast<const uint32_t *>(kr1)[i];
-    }
-#pragma unroll
-    for (int sg = 0; sg < 8; ++sg) {
-      const int kap = 32 * (sg >> 1) + 16 * (sg & 1) + 4 * q;
-      uint32_t lo, hi, p01, p23;
-      lookup<BK>(lkf, k_selector<BK>(wk0, sg), lo, hi);
-      f16_pairs(lo, hi, p01, p23);
-      *reinterpret_cast<uint2 *>(kt + sw_off(k0, kap)) = make_uint2(p01, p23);
-      lookup<BK>(lkf, k_selector<BK>(wk1, sg), lo, hi);
-      f16_pairs(lo, hi, p01, p23);
-      *reinterpret_cast<uint2 *>(kt + sw_off(k1, kap)) = make_uint2(p01, p23);
-    }
-  }
-#pragma unroll
-  for (int rb = 0; rb < 2; ++rb) {
-    // V~^T: rows in the V fragment order, keys as columns (decode's A
-    // fragments: a0 = row 16 mt + r, keys 2q, 2q+1; a1 = row + 8; a2, a3:
-    // keys + 8)
-    constexpr int VB = D * BV / 8;
-    const int kb = 32 * ew + 16 * rb;  // first key of the 16-key block
-    const unsigned char *vc = st + St::vc + (kb + 2 * q) * VB;
-    auto put = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-      *reinterpret_cast<uint32_t *>(vt + sw_off(16 * mt + r, kb + 2 * q)) = a0;
-      *reinterpret_cast<uint32_t *>(vt + sw_off(16 * mt + r + 8, kb + 2 * q)) = a1;
-      *reinterpret_cast<uint32_t *>(vt + sw_off(16 * mt + r, kb + 8 + 2 * q)) = a2;
-      *reinterpret_cast<uint32_t *>(vt + sw_off(16 * mt + r + 8, kb + 8 + 2 * q)) = a3;
-    };
-    if constexpr (BV == 3) {
-      const int gofs = 12 * (r >> 1);
-      const uint32_t gs = (r & 1) ? 0x7362u : 0x5140u;
-      uint32_t ya[3], yb[3];
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        ya[k] = prmt(reinterpret_cast<const uint32_t *>(vc + gofs)[k],
-                     reinterpret_cast<const uint32_t *>(vc + VB + gofs)[k], gs);
-        yb[k] = prmt(reinterpret_cast<const uint32_t *>(vc + 8 * VB + gofs)[k],
-                     reinterpret_cast<const uint32_t *>(vc + 9 * VB + gofs)[k], gs);
-      }
-      const uint32_t spa = spare3(ya[0], ya[1], ya[2]), spb = spare3(yb[0], yb[1], yb[2]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t za = k < 3 ? (ya[k < 3 ? k : 0] & 0x77777777u) : spa;
-        const uint32_t zb = k < 3 ? (yb[k < 3 ? k : 0] & 0x77777777u) : spb;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t a0, a1, a2, a3;
-          v_pairs<3>(lv, hh ? za >> 16 : za, a0, a1);
-          v_pairs<3>(lv, hh ? zb >> 16 : zb, a2, a3);
-          put(2 * k + hh, a0, a1, a2, a3);
-        }
-      }
-    } else if constexpr (BV == 2) {
-      const uint32_t A0 = reinterpret_cast<const uint32_t *>(vc)[r];
-      const uint32_t B0 = reinterpret_cast<const uint32_t *>(vc + VB)[r];
-      const uint32_t A1 = reinterpret_cast<const uint32_t *>(vc + 8 * VB)[r];
-      const uint32_t B1 = reinterpret_cast<const uint32_t *>(vc + 9 * VB)[r];
-#pragma unroll
-      for (int yh = 0; yh < 2; ++yh) {
-        const uint32_t gs = yh ? 0x7362u : 0x5140u;
-        const uint32_t ya = prmt(A0, B0, gs), yb = prmt(A1, B1, gs);
-#pragma unroll
-        for (int par = 0; par < 2; ++par) {
-          const uint32_t za = (ya >> (2 * par)) & 0x33333333u, zb = (yb >> (2 * par)) & 0x33333333u;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t a0, a1, a2, a3;
-            v_pairs<2>(lv, hh ? za >> 16 : za, a0, a1);
-            v_pairs<2>(lv, hh ? zb >> 16 : zb, a2, a3);
-            put(4 * yh + 2 * par + hh, a0, a1, a2, a3);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t A0 = reinterpret_cast<const uint32_t *>(vc)[2 * r + u];
-        const uint32_t B0 = reinterpret_cast<const uint32_t *>(vc + VB)[2 * r + u];
-        const uint32_t A1 = reinterpret_cast<const uint32_t *>(vc + 8 * VB)[2 * r + u];
-        const uint32_t B1 = reinterpret_cast<const uint32_t *>(vc + 9 * VB)[2 * r + u];
-#pragma unroll
-        for (int yh = 0; yh < 2; ++yh) {
-          const uint32_t gs = yh ? 0x7362u : 0x5140u;
-          const uint32_t ya = prmt(A0, B0, gs), yb = prmt(A1, B1, gs);
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t a0, a1, a2, a3;
-            v_pairs<4>(lv, hh ? ya >> 16 : ya, a0, a1);
-            v_pairs<4>(lv, hh ? yb >> 16 : yb, a2, a3);
-            put(4 * u + 2 * yh + hh, a0, a1, a2, a3);
-          }
-        }
-      }
-    }
-  }
 }
 
 // A wait on the kernel's flag or on a barrier; false (and the error flagged,
@@ -1065,14 +937,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const Prefill
   } else if (warp >= kTcExpWarp0) {
     // ---------------- expansion: K~ and V~ of every tile, double-buffered
     const int ew = warp - kTcExpWarp0;
-    Lut lkf;  // the K centroids as fp16 byte tables (exact: the centroids are fp16 values)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lkf.lo[i] = lkf.hi[i] = 0u;
-    for (int e = 0; e < (1 << BK); ++e) {
-      const uint16_t hb = __half_as_ushort(__float2half_rn(a.p.cb[e]));
-      lkf.lo[e / 4] |= (uint32_t)(hb & 0xff) << (8 * (e % 4));
-      lkf.hi[e / 4] |= (uint32_t)(hb >> 8) << (8 * (e % 4));
-    }
+    const Lut lkf = fp16_lut<BK>(a.p.cb);
     const Lut lv = a.p.lut_v;
     // the first expansion overwrites the softmax warps' q_hat scratch
     bool ok = tc_wait(&scratch_free, 0, err, abf);
@@ -1083,7 +948,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const Prefill
       if (!ok || *(volatile int *)abf) break;
       tcx_fence_after();
       const unsigned char *st = sm + L::ring + slot * L::stage;
-      expand_tile<BK, BV>(st, sm + (b ? L::kt1 : L::kt0), sm + (b ? L::vt1 : L::vt0), lkf, lv, ew, r, q);
+      expand_keys<BK, BV>(st, sm + (b ? L::kt1 : L::kt0), lkf, ew, r, q);
+      expand_values<BK, BV>(st, sm + (b ? L::vt1 : L::vt0), lv, ew, r, q);
       {  // the key norms as fp32 for the softmax warps (keys past the copied ones are masked there)
         const int key = tid - 32 * kTcExpWarp0;
         float *nf = reinterpret_cast<float *>(sm + L::nf) + b * 2 * kTcKeys;

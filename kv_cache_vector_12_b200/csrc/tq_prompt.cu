@@ -83,61 +83,12 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t block) {
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// D += A B with A in tensor memory and B in shared memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-               "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-               : "memory");
-}
-
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
-}
-
-// 32 consecutive 32-bit columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(t)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
-          r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
-      : "memory");
-}
-__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// After ld_wait: passes the loaded registers through an empty asm, so that no
-// use of them is scheduled above the wait.
-__device__ __forceinline__ void pin32(uint32_t (&r)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 16)
-    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                 "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
-                 "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -152,12 +103,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float f(uint32_t x) { return __uint_as_float(x); }
 
 // A bounded wait; false (the error flagged, the kernel told to stop) once it
-// expires.
-__device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, unsigned *err, int *stop) {
-  if (bar_wait(smem_addr(bar), parity)) return true;
+// expires.  Only the first test is inlined: the waits are many, and the loop
+// and its error path would crowd the instruction cache.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned *err, int *stop) {
+  if (bar_wait(bar, parity)) return true;
   atomicOr(err, kErrWaitExpired);
   *(volatile int *)stop = 1;
   return false;
+}
+__device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, unsigned *err, int *stop) {
+  const uint32_t b = smem_addr(bar);
+  return bar_try(b, parity) || wait_slow(b, parity, err, stop);
+}
+// The same by a whole warp: every lane leaves with the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned *err, int *stop) {
+  return __all_sync(0xffffffffu, wait_or_stop(bar, parity, err, stop));
 }
 
 // Query blocks (of `span` positions) of sequence s; 0 for a sequence outside
@@ -234,7 +194,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int stop, s_seq, s_blk;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+  const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31, h = blockIdx.y;
   const int G = a.n_q_heads / a.n_kv_heads, PC = a.per_tile, span = NT * PC;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {
@@ -267,7 +227,8 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  // all 512 columns are this CTA's: the base is column 0 of lane 0
+  constexpr uint32_t tmem = 0;
   const int s = s_seq;
 
   if (s >= 0) {
@@ -310,72 +271,74 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
         }
       }
     } else if (warp == C::kMmaWarp) {
-      // ---------------- MMA issuer
-      if (lane == 0) {
-        auto slot_addr = [&](int it) { return smem_addr(ring + (it % C::kSlots) * C::kSlot); };
-        auto loaded = [&](int it) {
-          return wait_or_stop(&full[it % C::kSlots], (it / C::kSlots) & 1, a.err, &stop);
-        };
-        auto scores = [&](int i, int buf, int j) {  // row tile i, tensor-memory buffer buf, key tile j
-          const uint32_t q = smem_addr(sm + i * C::kQTile), k = slot_addr(2 * j);
+      // ---------------- MMA issuer (the whole warp; one lane issues)
+      auto slot_desc = [&](int it) { return smem_addr(ring + (it % C::kSlots) * C::kSlot); };
+      auto loaded = [&](int it) { return warp_wait(&full[it % C::kSlots], (it / C::kSlots) & 1, a.err, &stop); };
+      auto scores = [&](int i, int buf, int j) {  // row tile i, tensor-memory buffer buf, key tile j
+        const uint64_t q = sw128_desc(smem_addr(sm + i * C::kQTile)), k = sw128_desc(slot_desc(2 * j));
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk)
-            tc_mma_n(tmem + C::s_col(buf), sw128_desc(q + (kk >> 2) * C::kQBox + (kk & 3) * 32),
-                     sw128_desc(k + (kk >> 2) * C::kKVBox + (kk & 3) * 32), C::idesc_s, kk > 0);
-        };
-        auto values = [&](int i, int buf, int j) {
-          const uint32_t v = slot_addr(2 * j + 1);
+        for (int kk = 0; kk < DH / 16; ++kk)
+          tc_mma_n(tmem + C::s_col(buf), q + (((kk >> 2) * C::kQBox + (kk & 3) * 32) >> 4),
+                   k + (((kk >> 2) * C::kKVBox + (kk & 3) * 32) >> 4), C::idesc_s, kk > 0);
+      };
+      auto values = [&](int i, int buf, int j) {
+        const uint64_t v = mn_desc(slot_desc(2 * j + 1), C::kKVBox);
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            mma_ts(tmem + C::o_col(i), tmem + C::p_col(buf) + 8 * kk, mn_desc(v + kk * 2048, C::kKVBox), C::idesc_o,
-                   (j > 0 || kk > 0) ? 1u : 0u);
-        };
-        bool ok = wait_or_stop(&q_full, 0, a.err, &stop) && loaded(0);
-        if (ok) {
-          tc_fence_after();
-          if constexpr (NT == 2) {
+        for (int kk = 0; kk < KT / 16; ++kk)  // 16 tokens: 2048 bytes
+          mma_ts(tmem + C::o_col(i), tmem + C::p_col(buf) + 8 * kk, v + kk * (2048 >> 4), C::idesc_o,
+                 (j > 0 || kk > 0) ? 1u : 0u);
+      };
+      bool ok = warp_wait(&q_full, 0, a.err, &stop) && loaded(0);
+      if (ok) {
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (tiles[i] > 0) {
-                scores(i, i, 0);
-                tc_commit(smem_addr(&s_full[i]));
-              }
-          } else {
-            scores(0, 0, 0);
-            tc_commit(smem_addr(&s_full[0]));
-          }
+          for (int i = 0; i < NT; ++i)
+            if (tiles[i] > 0) {
+              scores(i, i, 0);
+              tc_commit(smem_addr(&s_full[i]));
+            }
           tc_commit(smem_addr(&empty[0]));
         }
-        for (int j = 0; ok && j < n_tiles; ++j) {
-          const bool more = j + 1 < n_tiles;
-          if constexpr (NT == 1) {
-            if (more) {
-              ok = loaded(2 * j + 2);
-              if (!ok || *(volatile int *)&stop) break;
-              // S and P buffer (j + 1) % 2 were last used by tile j - 1, whose
-              // weights were complete before its value MMAs were issued
+        __syncwarp();
+      }
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        const bool more = j + 1 < n_tiles;
+        if constexpr (NT == 1) {
+          if (more) {
+            ok = loaded(2 * j + 2);
+            if (!ok || *(volatile int *)&stop) break;
+            // S and P buffer (j + 1) % 2 were last used by tile j - 1, whose
+            // weights were complete before its value MMAs were issued
+            if (elect_one()) {
               scores(0, (j + 1) & 1, j + 1);
               tc_commit(smem_addr(&s_full[(j + 1) & 1]));
               tc_commit(smem_addr(&empty[(2 * j + 2) % C::kSlots]));
             }
-            ok = loaded(2 * j + 1) && wait_or_stop(&p_full[j & 1], (j >> 1) & 1, a.err, &stop);
-            if (!ok || *(volatile int *)&stop) break;
-            tc_fence_after();
+            __syncwarp();
+          }
+          ok = loaded(2 * j + 1) && warp_wait(&p_full[j & 1], (j >> 1) & 1, a.err, &stop);
+          if (!ok || *(volatile int *)&stop) break;
+          tc_fence_after();
+          if (elect_one()) {
             values(0, j & 1, j);
             tc_commit(smem_addr(&o_full[0]));
             if (!more) tc_commit(smem_addr(&o_full[1]));
             tc_commit(smem_addr(&empty[(2 * j + 1) % C::kSlots]));
-          } else {
-            // O += P V of tile j, then S of tile j + 1 (over the P just read:
-            // MMAs of one thread run in order), for each row tile in turn
-            ok = loaded(2 * j + 1) && (!more || loaded(2 * j + 2));
-            if (!ok || *(volatile int *)&stop) break;
+          }
+          __syncwarp();
+        } else {
+          // O += P V of tile j, then S of tile j + 1 (over the P just read:
+          // MMAs of one thread run in order), for each row tile in turn
+          ok = loaded(2 * j + 1) && (!more || loaded(2 * j + 2));
+          if (!ok || *(volatile int *)&stop) break;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (j >= tiles[i]) continue;
-              ok = ok && wait_or_stop(&p_full[i], j & 1, a.err, &stop);
-              if (!ok) break;
-              tc_fence_after();
+          for (int i = 0; i < 2; ++i) {
+            if (j >= tiles[i]) continue;
+            ok = ok && warp_wait(&p_full[i], j & 1, a.err, &stop);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
               values(i, i, j);
               if (j + 1 < tiles[i]) {
                 scores(i, i, j + 1);
@@ -384,15 +347,20 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
                 tc_commit(smem_addr(&o_full[i]));
               }
             }
-            if (!ok || *(volatile int *)&stop) break;
+            __syncwarp();
+          }
+          if (!ok || *(volatile int *)&stop) break;
+          if (elect_one()) {
             tc_commit(smem_addr(&empty[(2 * j + 1) % C::kSlots]));
             if (more) tc_commit(smem_addr(&empty[(2 * j + 2) % C::kSlots]));
           }
+          __syncwarp();
         }
-        // every MMA issued here has completed before the tensor memory is released
-        tc_commit(smem_addr(&fin));
-        bar_wait(smem_addr(&fin), 0);
       }
+      // every MMA issued here has completed before the tensor memory is released
+      if (elect_one()) tc_commit(smem_addr(&fin));
+      __syncwarp();
+      bar_wait(smem_addr(&fin), 0);
     } else {
       // ---------------- softmax: row tile i, one thread per row
       const int i = NT == 2 ? warp >> 2 : 0, row = tid & 127;
@@ -405,7 +373,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
       for (int j = 0; j < n; ++j) {
         const int buf = NT == 2 ? i : (j & 1);
         const uint32_t par = NT == 2 ? (j & 1) : ((j >> 1) & 1);
-        ok = wait_or_stop(&s_full[buf], par, a.err, &stop);
+        ok = warp_wait(&s_full[buf], par, a.err, &stop);
         if (!ok || *(volatile int *)&stop) {
           ok = false;
           break;
@@ -438,7 +406,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
           const bool move = mx > ref + kLazy;
           if (__any_sync(0xffffffffu, move)) {
             if constexpr (NT == 1) {
-              ok = wait_or_stop(&o_full[0], (j - 1) & 1, a.err, &stop);
+              ok = warp_wait(&o_full[0], (j - 1) & 1, a.err, &stop);
               if (!ok) break;
               tc_fence_after();
             }
@@ -480,7 +448,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
           // the tile's rows behind the sequence's end hold other tokens: zero
           // them, so that a weight of 0 times what they hold stays 0
           const int vs = 2 * j + 1;
-          ok = wait_or_stop(&full[vs % C::kSlots], (vs / C::kSlots) & 1, a.err, &stop);
+          ok = warp_wait(&full[vs % C::kSlots], (vs / C::kSlots) & 1, a.err, &stop);
           if (!ok) break;
           unsigned char *vt = ring + (vs % C::kSlots) * C::kSlot;
           for (int x = 128 * (len - key0) + 16 * row; x < C::kKVBox; x += 128 * 16)
@@ -495,7 +463,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
       if (ok && n > 0) {
         // (with NT == 1 o_full[0] takes a phase per tile, of which this thread
         // may be two behind, so the last tile has a barrier of its own)
-        ok = wait_or_stop(&o_full[NT == 2 ? i : 1], 0, a.err, &stop);
+        ok = warp_wait(&o_full[NT == 2 ? i : 1], 0, a.err, &stop);
         if (ok) {
           tc_fence_after();
           const float il = 1.f / l;
@@ -533,7 +501,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
   __syncthreads();
   if (warp == C::kMmaWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(512u) : "memory");
   }
 }
 

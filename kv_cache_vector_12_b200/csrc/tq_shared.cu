@@ -12,15 +12,19 @@
 // partials, rotates back (Pi^T) and rounds to the output's type once.
 //
 // The passes are the decode attention kernel in its SHARED build
-// (tq_decode_kernel.cuh): up to 16 rows per CTA.
+// (tq_decode_kernel.cuh), up to 16 rows per CTA; groups of more rows at d = 128
+// without QJL take the prefix pass of tq_shared_tc.cu, up to 128 rows per CTA.
 #include <cmath>
 
 #include "tq_decode_kernel.cuh"
 #include "tq_merge.cuh"
+#include "tq_shared_tc.h"
 
 namespace tq {
 namespace {
 
+constexpr int kTcMinRows = 16;   // rows of a group above which the tcgen05 prefix pass runs
+constexpr int kTcFixed = 4;
 constexpr int kMaxSlots = 1024;  // split partials of one row, both passes
 
 struct MergeArgs {
@@ -104,12 +108,28 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
                        int max_group, int max_prefix, int max_suffix) {
   SharedPlan s = {};
   const int per = n_q_heads / n_kv_heads;
+  s.tc = d == kHeadDim && !qjl && (long)per * max_group > kTcMinRows;
   s.nt_p = (long)per * max_group > 8 ? 2 : 1;
-  s.members = 8 * s.nt_p / per;
+  s.members = (s.tc ? 128 : 8 * s.nt_p) / per;
   const long by_group = (long)n_groups * ((max_group + s.members - 1) / s.members);
   const long by_seq = (long)n_seqs / s.members + n_groups;
   s.units = (int)(by_group < by_seq ? by_group : by_seq);
-  if (max_prefix > 0) {
+  if (max_prefix > 0 && s.tc) {
+    // splits of whole 128-key tiles, one CTA per SM: the count with the fewest
+    // tile times over all waves, kTcFixed of them per CTA for its prologue
+    // (q rotation) and its partial
+    const long tiles = (max_prefix + 127) / 128, lanes = (long)s.units * n_kv_heads, sms = sm_count();
+    long best = -1;
+    for (long n = 1; n <= tiles && n <= 128; ++n) {
+      const long per_split = (tiles + n - 1) / n, used = (tiles + per_split - 1) / per_split;
+      const long cost = (lanes * used + sms - 1) / sms * (per_split + kTcFixed);
+      if (best < 0 || cost < best) {
+        best = cost;
+        s.p_chunk = (int)(per_split * 128);
+        s.p_splits = (int)used;
+      }
+    }
+  } else if (max_prefix > 0) {
     const DecodeSplit sp =
         decode_split(s.units, n_kv_heads, max_prefix, shared_ctas_per_sm(d, bits_k, bits_v, qjl, s.nt_p));
     s.p_chunk = sp.chunk;
@@ -156,7 +176,14 @@ int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q
   args.max_suffix = max_suffix;
   args.members = plan.members;
   cfg.blockDim = dim3(kThreads);
-  if (plan.p_splits > 0) {
+  if (plan.p_splits > 0 && plan.tc) {
+    const SharedTcArgs t{p,         c,        n_q_heads,  q,            q_dtype,      scale,         cu_group, prefix,
+                         n_groups, max_group, max_prefix, plan.members, plan.p_chunk, args.partials, args.n_splits};
+    cfg.gridDim = dim3(plan.p_splits, c.n_kv_heads, plan.units);
+    const int e = launch_shared_prefix_tc(t, cfg);
+    if (e != 0) return e;
+    cfg.blockDim = dim3(kThreads);
+  } else if (plan.p_splits > 0) {
     shared_ctas_per_sm(p.d, p.bits_k, p.bits_v, p.qjl, plan.nt_p);  // sets the kernel's shared memory
     const DecodeVariant v = shared_kernel(p, plan.nt_p);
     args.pass = kPassPrefix;
