@@ -356,24 +356,29 @@ tq_status tq_create_ex(tq_ctx **out, int32_t d, int32_t bits_k, int32_t bits_v, 
     delete ctx;
     return cuda_fail(e, "cudaGetDevice");
   }
-  uint8_t kperm[256], vperm[256], jperm[256];
+  uint8_t kperm[256], vperm[256], jperm[256], kvperm[256], vpos[256];
   tq::kperm_of(bits_k, d, kperm);
   tq::vperm_of(bits_v, d, vperm);
   tq::jperm_of(d, jperm);
+  // V's codes expanded in the K fragment order (of bits_v), by V order position
+  tq::kperm_of(bits_v, d, kvperm);
+  for (int k = 0; k < d; ++k) vpos[vperm[k]] = (uint8_t)k;
+  for (int k = 0; k < d; ++k) kvperm[k] = vpos[kvperm[k]];
   ctx->dp.k_shift = k_fixed_shift(ctx->ck.data(), bits_k);
   if (!is_permutation(kperm, d) || !is_permutation(vperm, d) || !is_permutation(jperm, d) ||
+      !is_permutation(kvperm, d) ||
       !build_luts(ctx->ck.data(), bits_k, ctx->dp.k_shift, ctx->cv.data(), bits_v, ctx->dp.lut_k, ctx->dp.lut_v)) {
     delete ctx;
     return fail(TQ_ERR_UNSUPPORTED, "internal: fragment orders or codebook tables could not be built");
   }
-  // One block: pi | pik | pivt | pif | pvf | s | sjkf | sf | ssplit | codebooks | kperm | jperm | error word.
+  // One block: pi | pik | pivt | pif | pvf | s | sjkf | sf | ssplit | codebooks | kperm | jperm | kvperm | error word.
   const size_t dd = (size_t)d * d;
   const size_t off_pi = 0, off_pik = off_pi + dd * 2, off_piv = off_pik + dd * 2, off_pif = off_piv + dd * 2;
   const size_t off_pvf = off_pif + dd * 2, off_s = off_pvf + dd * 2;
   const size_t off_sjk = off_s + dd * 4, off_sf = off_sjk + dd * 4, off_ss = off_sf + 2 * dd * 2;
   const size_t off_cb = off_ss + 2 * dd * 2;
   const size_t off_kperm = off_cb + 4 * tq::kMaxLevels * 4, off_jperm = off_kperm + 256;
-  const size_t off_err = off_jperm + 256, total = off_err + 256;
+  const size_t off_kvperm = off_jperm + 256, off_err = off_kvperm + 256, total = off_err + 256;
   e = cudaMalloc(&ctx->dev_block, total);
   if (e != cudaSuccess) {
     delete ctx;
@@ -431,6 +436,7 @@ tq_status tq_create_ex(tq_ctx **out, int32_t d, int32_t bits_k, int32_t bits_v, 
   tq::mma_b_fragments(pivt, d, (uint32_t *)(h.data() + off_pvf));
   std::memcpy(h.data() + off_kperm, kperm, (size_t)d);
   std::memcpy(h.data() + off_jperm, jperm, (size_t)d);
+  std::memcpy(h.data() + off_kvperm, kvperm, (size_t)d);
   float *cb = (float *)(h.data() + off_cb);
   std::memcpy(cb + 0 * tq::kMaxLevels, ctx->ck.data(), tq::kMaxLevels * 4);
   std::memcpy(cb + 1 * tq::kMaxLevels, ctx->tk.data(), tq::kMaxLevels * 4);
@@ -456,6 +462,7 @@ tq_status tq_create_ex(tq_ctx **out, int32_t d, int32_t bits_k, int32_t bits_v, 
   ctx->dp.pvf = (const uint32_t *)(base + off_pvf);
   ctx->dp.kperm = (const uint8_t *)(base + off_kperm);
   ctx->dp.jperm = (const uint8_t *)(base + off_jperm);
+  ctx->dp.kvperm = (const uint8_t *)(base + off_kvperm);
   ctx->dp.d = d;
   ctx->dp.bits_k = bits_k;
   ctx->dp.bits_v = bits_v;

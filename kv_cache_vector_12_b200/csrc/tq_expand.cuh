@@ -26,71 +26,64 @@ __device__ __forceinline__ void f16_pairs(uint32_t lo, uint32_t hi, uint32_t &p0
   p23 = prmt(lo, hi, 0x7362u);
 }
 
-// K~[key][kappa] of keys kb .. kb + 15 of a tile (the K centroids in fp16, K
-// fragment order) into kt, by one warp (r = lane / 4, q = lane % 4).
-template <int BK, int BV>
-__device__ __forceinline__ void expand_keys16(const unsigned char *st, unsigned char *kt, const Lut &lkf, int kb, int r,
-                                              int q) {
-  using St = Stage<BK, BV, false, kTcKeys>;
+// X~[key][kappa] of keys kb .. kb + 15 of a tile (the table's entries of B-bit
+// codes, rows of D B / 8 bytes from `codes`, K fragment order) into xt, by one
+// warp (r = lane / 4, q = lane % 4).  SCALED: times the keys' norms, rounded to
+// fp16 once; keys at or past `left` become 0, whatever their norms hold.
+template <int B, bool SCALED = false>
+__device__ __forceinline__ void expand_rows16(const unsigned char *codes, unsigned char *xt, const Lut &lut, int kb,
+                                              int r, int q, const __half *norms = nullptr, int left = kTcKeys) {
   // rows 0 2 4 6 1 3 5 7 by r: the four rows of a half-warp's 8-byte stores then
   // fall on different pairs of swizzled 16-byte chunks (in natural order two
   // and two share a pair, which halves the store rate)
   const int k0 = kb + (((r << 1) & 6) | (r >> 2)), k1 = k0 + 8;
-  uint32_t wk0[BK], wk1[BK];
-  const unsigned char *kr0 = st + St::kc + k0 * (D * BK / 8) + q * 4 * BK;
-  const unsigned char *kr1 = st + St::kc + k1 * (D * BK / 8) + q * 4 * BK;
+  uint32_t wk0[B], wk1[B];
+  const unsigned char *kr0 = codes + k0 * (D * B / 8) + q * 4 * B;
+  const unsigned char *kr1 = codes + k1 * (D * B / 8) + q * 4 * B;
 #pragma unroll
-  for (int i = 0; i < BK; ++i) {
+  for (int i = 0; i < B; ++i) {
     wk0[i] = reinterpret_cast<const uint32_t *>(kr0)[i];
     wk1[i] = reinterpret_cast<const uint32_t *>(kr1)[i];
   }
+  __half2 n0, n1;
+  if constexpr (SCALED) {
+    const __half z = __ushort_as_half(0);
+    n0 = __half2half2(k0 < left ? norms[k0] : z);
+    n1 = __half2half2(k1 < left ? norms[k1] : z);
+  }
+  auto put = [&](int key, int kap, uint32_t sel, __half2 n) {
+    uint32_t lo, hi, p01, p23;
+    lookup<B>(lut, sel, lo, hi);
+    f16_pairs(lo, hi, p01, p23);
+    if constexpr (SCALED) {
+      auto times = [&](uint32_t x) {
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x), n);
+        return *reinterpret_cast<const uint32_t *>(&y);
+      };
+      p01 = times(p01), p23 = times(p23);
+    }
+    *reinterpret_cast<uint2 *>(xt + sw_off(key, kap)) = make_uint2(p01, p23);
+  };
 #pragma unroll
   for (int sg = 0; sg < 8; ++sg) {
     const int kap = 32 * (sg >> 1) + 16 * (sg & 1) + 4 * q;
-    uint32_t lo, hi, p01, p23;
-    lookup<BK>(lkf, k_selector<BK>(wk0, sg), lo, hi);
-    f16_pairs(lo, hi, p01, p23);
-    *reinterpret_cast<uint2 *>(kt + sw_off(k0, kap)) = make_uint2(p01, p23);
-    lookup<BK>(lkf, k_selector<BK>(wk1, sg), lo, hi);
-    f16_pairs(lo, hi, p01, p23);
-    *reinterpret_cast<uint2 *>(kt + sw_off(k1, kap)) = make_uint2(p01, p23);
+    put(k0, kap, k_selector<B>(wk0, sg), n0);
+    put(k1, kap, k_selector<B>(wk1, sg), n1);
   }
 }
 
-// V~^T[kappa_v][key] of keys kb .. kb + 15 (the table's fp16 entries, V
-// fragment order) into vt.  SCALED: times the keys' value norms, rounded to
-// fp16 once; keys at or past `left` become 0, whatever their norms hold.
-template <int BK, int BV, bool SCALED = false>
+// V~^T[kappa_v][key] of keys kb .. kb + 15 (fp16 V centroids, V fragment
+// order) into vt.
+template <int BK, int BV>
 __device__ __forceinline__ void expand_values16(const unsigned char *st, unsigned char *vt, const Lut &lv, int kb,
-                                                int r, int q, int left = kTcKeys) {
+                                                int r, int q) {
   using St = Stage<BK, BV, false, kTcKeys>;
-  __half2 n0, n1;  // norms of keys kb + 2 q (+ 1) and kb + 2 q + 8 (+ 9)
-  if constexpr (SCALED) {
-    const __half2 *vn = reinterpret_cast<const __half2 *>(st + St::vn) + kb / 2 + q;
-    n0 = vn[0];
-    n1 = vn[4];
-    const int k = kb + 2 * q;
-    if (k + 9 >= left) {
-      const __half z = __ushort_as_half(0);
-      if (k >= left) n0 = __halves2half2(z, z);
-      else if (k + 1 >= left) n0 = __halves2half2(__low2half(n0), z);
-      if (k + 8 >= left) n1 = __halves2half2(z, z);
-      else n1 = __halves2half2(__low2half(n1), z);
-    }
-  }
   // V~^T: rows in the V fragment order, keys as columns (decode's A
   // fragments: a0 = row 16 mt + r, keys 2q, 2q+1; a1 = row + 8; a2, a3:
   // keys + 8)
   constexpr int VB = D * BV / 8;
   const unsigned char *vc = st + St::vc + (kb + 2 * q) * VB;
   auto put = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-    if constexpr (SCALED) {
-      auto times = [](uint32_t x, __half2 n) {
-        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x), n);
-        return *reinterpret_cast<const uint32_t *>(&y);
-      };
-      a0 = times(a0, n0), a1 = times(a1, n0), a2 = times(a2, n1), a3 = times(a3, n1);
-    }
     *reinterpret_cast<uint32_t *>(vt + sw_off(16 * mt + r, kb + 2 * q)) = a0;
     *reinterpret_cast<uint32_t *>(vt + sw_off(16 * mt + r + 8, kb + 2 * q)) = a1;
     *reinterpret_cast<uint32_t *>(vt + sw_off(16 * mt + r, kb + 8 + 2 * q)) = a2;
@@ -164,12 +157,13 @@ __device__ __forceinline__ void expand_values16(const unsigned char *st, unsigne
   }
 }
 
-// The same for the 32 keys of warp ew (0-3).
+// K~ and V~^T of the 32 keys of warp ew (0-3).
 template <int BK, int BV>
 __device__ __forceinline__ void expand_keys(const unsigned char *st, unsigned char *kt, const Lut &lkf, int ew, int r,
                                             int q) {
 #pragma unroll
-  for (int rb = 0; rb < 2; ++rb) expand_keys16<BK, BV>(st, kt, lkf, 32 * ew + 16 * rb, r, q);
+  for (int rb = 0; rb < 2; ++rb)
+    expand_rows16<BK>(st + Stage<BK, BV, false, kTcKeys>::kc, kt, lkf, 32 * ew + 16 * rb, r, q);
 }
 template <int BK, int BV>
 __device__ __forceinline__ void expand_values(const unsigned char *st, unsigned char *vt, const Lut &lv, int ew, int r,

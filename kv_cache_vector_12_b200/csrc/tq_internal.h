@@ -62,6 +62,7 @@ struct DeviceParams {
   unsigned *err;          // sticky error flags
   const uint8_t *kperm;   // [d] K fragment order -> coordinate
   const uint8_t *jperm;   // [d] QJL fragment order -> projection index
+  const uint8_t *kvperm;  // [d] position in V's codes read in K fragment order -> position in V fragment order
   const uint16_t *pivt;   // [d][d] bf16: pivt[i][k] = Pi[vperm[k]][i] (Pi^T, columns in V fragment order)
   const uint32_t *pvf;    // pivt as bf16 MMA B fragments, laid out like pif (the product O pivt^T)
   Lut lut_k, lut_v;

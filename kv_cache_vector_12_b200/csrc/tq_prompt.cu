@@ -76,13 +76,6 @@ struct PromptArgs {
   float *lse;                           // [n_tok][n_q_heads] or null
 };
 
-// MN-major shared-memory descriptor of V: 128-byte swizzle, 64-column blocks
-// `block` bytes apart, groups of eight tokens 1024 bytes apart.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t block) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(

@@ -4,16 +4,17 @@
 //
 // Keys are expanded in tiles of 128 and attended in halves of 64; four roles
 // overlap across them:
-//   expand   (8 warps, 16 keys of a tile each) K~ and (||v|| V~)^T from the
-//            codes, as fp16 operands in shared memory, each double-buffered;
+//   expand   (8 warps, 16 keys of a tile each) K~ and ||v|| V~ from the
+//            codes, token by token, as fp16 operands in shared memory, each
+//            double-buffered (V~ is an MN-major operand: no transpose);
 //   MMA      (1 thread) S = Q^_hi K~^T + Q^_lo K~^T (two-part fp16 q_hat in
 //            tensor memory, about 22 bits), O += P (||v|| V~) with P in tensor
 //            memory over the S it came from; S is double-buffered;
-//   softmax  (2 x 4 warps, one thread per row) the two sets take the halves in
+//   softmax  (4 x 4 warps, one thread per row) the sets take the halves in
 //            turn: S from tensor memory, exp2 against the row's reference, P as
 //            fp16 back;
 //   producer (1 thread) the packed planes by bulk copies.
-// A row's reference r is handed from half to half between the two sets.  It
+// A row's reference r is handed from half to half between the sets.  It
 // moves, and O is rescaled, only when a half's maximum may pass it by more than
 // kLazy log2 units (p <= 2^kLazy stays far inside fp16): the test takes
 // max S times the half's largest key norm, a bound, and only when the bound
@@ -42,7 +43,9 @@ namespace {
 constexpr float kLazy = 8.f;
 constexpr float kVScale = 4.f;
 constexpr int kHalf = 64, kBufs = 4;  // keys per S buffer, S buffers
-constexpr int kSoftWarps = 8, kExpWarps = 8;
+// warps: four softmax sets, expansion, the producer and the MMA issuer; 26 warps
+// leave 72 registers a thread
+constexpr int kSets = 4, kSoftWarps = 4 * kSets, kExpWarps = 8;
 constexpr int kExpWarp0 = kSoftWarps, kProdWarp = kExpWarp0 + kExpWarps, kMmaWarp = kProdWarp + 1;
 constexpr int kTcThreads = 32 * (kMmaWarp + 1);
 constexpr int kStagesTc = 4, kNormBufs = 4;
@@ -59,8 +62,9 @@ struct SharedTc {
 
 // kind::f16, fp32 accumulator, M = N = 128, A and B K-major: fp16 inputs
 // (scores, values) and bf16 (the q rotation).
-constexpr uint32_t kDescO = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t kDescQ = kDescO | (1u << 7) | (1u << 10);
+constexpr uint32_t kDescS = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kDescO = kDescS | (1u << 16);  // (V~ by tokens: B is MN-major)
+constexpr uint32_t kDescQ = kDescS | (1u << 7) | (1u << 10);
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
@@ -96,9 +100,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
   unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ __align__(8) uint64_t full[kStagesTc], empty[kStagesTc];
   __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2];
-  __shared__ __align__(8) uint64_t p_full[kBufs], pv_done[kBufs];
-  __shared__ __align__(8) uint64_t checked[4][2], q_mma, q_ready, fin;
-  __shared__ float s_ref[128], s_fq[128], s_l[2][128], s_lref[2][128];
+  __shared__ __align__(8) uint64_t p_full[kBufs], pv_done[kBufs], n_full[kNormBufs];
+  __shared__ __align__(8) uint64_t checked[4][kSets], q_mma, q_ready, fin;
+  __shared__ float s_ref[128], s_fq[128], s_l[kSets][128], s_lref[kSets][128];
   __shared__ float s_kmax[kNormBufs][kExpWarps];  // largest key norm of each warp's 16 keys
   __shared__ uint32_t tmem_slot;
   __shared__ int stop;
@@ -106,6 +110,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
   const int split = blockIdx.x, h = blockIdx.y;
   const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
   const int per = a.n_q_heads / a.c.n_kv_heads;
+  // Pi's rows in the K fragment order, the B operand of q_hat = Pi q, into
+  // V~ of tile 1 (parameters: read before the kernels in front have ended)
+  for (int i = tid; i < 128 * 16; i += kTcThreads) {
+    const int row = i >> 4, c = 8 * (i & 15);
+    *reinterpret_cast<uint4 *>(sm + L::vt + kOpBytes + sw_off(row, c)) =
+        *reinterpret_cast<const uint4 *>(a.p.pi + (size_t)a.p.kperm[row] * D + c);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const SharedUnit u = find_members(a.cu_group, a.n_groups, a.max_group, a.members, a.c.n_seqs, blockIdx.z, lane);
   if (u.count == 0) return;
@@ -130,12 +141,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
       mbar_init(smem_u32(&k_empty[b]), 1);
       mbar_init(smem_u32(&v_empty[b]), 1);
       mbar_init(smem_u32(&s_full[b]), 1);
-      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&checked[w][b]), 1);
     }
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(smem_u32(&p_full[b]), 4);
       mbar_init(smem_u32(&pv_done[b]), 1);
     }
+    for (int b = 0; b < kNormBufs; ++b) mbar_init(smem_u32(&n_full[b]), kExpWarps);
+    for (int b = 0; b < kSets; ++b)
+      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&checked[w][b]), 1);
     mbar_init(smem_u32(&q_mma), 1);
     mbar_init(smem_u32(&q_ready), 4);
     mbar_init(smem_u32(&fin), 1);
@@ -148,35 +161,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // q_hat = Pi q is one pair of MMAs: q's rows (bf16; fp32 q as hi + lo) and
-  // Pi's rows in the K fragment order go into the buffers of tile 1 (lo: into
-  // K~ of tile 0)
+  // q's rows (bf16; fp32 q as hi + lo) into K~ of tile 1 (lo: of tile 0)
   const bool f32 = a.q_dtype == TQ_F32;
-  {
-    unsigned char *q_hi = sm + L::kt + kOpBytes, *q_lo = sm + L::kt, *pi = sm + L::vt + kOpBytes;
-    for (int i = tid; i < 128 * 16; i += kTcThreads) {
-      const int row = i >> 4, c = 8 * (i & 15);
-      uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-      if (row < rows) {
-        const long at = ((long)(u.first + row / per) * a.n_q_heads + h * per + row % per) * D + c;
-        if (f32) {
-          const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at);
-          const float4 x = src[0], y = src[1];
-          split_bf16x2(x.x, x.y, hi.x, lo.x);
-          split_bf16x2(x.z, x.w, hi.y, lo.y);
-          split_bf16x2(y.x, y.y, hi.z, lo.z);
-          split_bf16x2(y.z, y.w, hi.w, lo.w);
-        } else {
-          hi = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at);
-        }
+  for (int i = tid; i < 128 * 16; i += kTcThreads) {
+    const int row = i >> 4, c = 8 * (i & 15);
+    uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+    if (row < rows) {
+      const long at = ((long)(u.first + row / per) * a.n_q_heads + h * per + row % per) * D + c;
+      if (f32) {
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at);
+        const float4 x = src[0], y = src[1];
+        split_bf16x2(x.x, x.y, hi.x, lo.x);
+        split_bf16x2(x.z, x.w, hi.y, lo.y);
+        split_bf16x2(y.x, y.y, hi.z, lo.z);
+        split_bf16x2(y.z, y.w, hi.w, lo.w);
+      } else {
+        hi = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at);
       }
-      *reinterpret_cast<uint4 *>(q_hi + sw_off(row, c)) = hi;
-      if (f32) *reinterpret_cast<uint4 *>(q_lo + sw_off(row, c)) = lo;
-      *reinterpret_cast<uint4 *>(pi + sw_off(row, c)) =
-          *reinterpret_cast<const uint4 *>(a.p.pi + (size_t)a.p.kperm[row] * D + c);
     }
-    fence_async();
+    *reinterpret_cast<uint4 *>(sm + L::kt + kOpBytes + sw_off(row, c)) = hi;
+    if (f32) *reinterpret_cast<uint4 *>(sm + L::kt + sw_off(row, c)) = lo;
   }
+  fence_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
   constexpr uint32_t tmem = 0;
 
   if (warp < kSoftWarps) {
-    // ---------------- softmax: set w takes halves w, w + 2, ...
+    // ---------------- softmax: set w takes halves w, w + 4, ...
     const int w = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const bool idle = 32 * quarter >= rows;  // no row of this warp is in use
@@ -229,11 +235,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
     ok = ok && warp_wait(&q_ready, 0, err, &stop);
     const float fq = ok && !idle ? s_fq[row] : 0.f;
     float l = 0.f, mine = 0.f;  // the sum, and the reference it is relative to
-    for (int i = w; ok && i < n_half; i += 2) {
+    for (int i = w; ok && i < n_half; i += kSets) {
       const int t = i >> 1, buf = i & (kBufs - 1);
       const uint32_t t_s = tmem + kColS + kHalf * buf + lanes;
-      // the half's key norms (published with K~) and S
-      ok = warp_wait(&k_full[t & 1], (t >> 1) & 1, err, &stop) &&
+      // the half's key norms and S.  (The norms have barriers of their own:
+      // K~ of tile t + 2 may be complete before this set looks for tile t, and
+      // a wait on k_full would then be a phase behind.)
+      ok = warp_wait(&n_full[t % kNormBufs], (t / kNormBufs) & 1, err, &stop) &&
            warp_wait(&s_full[t & 1], (t >> 1) & 1, err, &stop);
       if (!ok || *(volatile int *)&stop) {
         ok = false;
@@ -241,48 +249,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
       }
       if (!idle) {
         tc_fence_after();
-        const float4 *kn = reinterpret_cast<const float4 *>(sm + L::norms) + (t % kNormBufs) * (kTcKeys / 4) + 16 * w;
+        const float4 *kn = reinterpret_cast<const float4 *>(sm + L::norms) + (t % kNormBufs) * (kTcKeys / 4) + 16 * (i & 1);
         const int left = t1 - t0 - i * kHalf;  // keys of this half in the split
-        uint32_t v[2][32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(t_s + 32 * c, v[c]);
-        ld_wait();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) pin32(v[c]);
-        if (left < kHalf) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
+        // S is read from tensor memory again wherever it is used: 32 columns at a
+        // time fit the registers that 26 warps leave
+        auto load = [&](int c, uint32_t (&v)[32]) {
+          tmem_ld32(t_s + 32 * c, v);
+          ld_wait();
+          pin32(v);
+          if (left < kHalf) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= left) v[c][e] = 0xff800000u;
-        }
+              if (32 * c + e >= left) v[e] = 0xff800000u;
+          }
+        };
         float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+          load(c, v);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) mx = max3(mx, f(v[c][e]), f(v[c][e + 1]));
-        const float *km = s_kmax[t % kNormBufs] + 4 * w;
+          for (int e = 0; e < 32; e += 2) mx = max3(mx, f(v[e]), f(v[e + 1]));
+        }
+        const float *km = s_kmax[t % kNormBufs] + 4 * (i & 1);
         const float bound = fmaxf(mx, 0.f) * fmaxf(fmaxf(km[0], km[1]), fmaxf(km[2], km[3])) * fq;
-        // the reference, handed over by the other set's check of half i - 1
+        // the reference, handed over by the check of half i - 1
         float ref = -INFINITY;
         if (i > 0) {
-          ok = warp_wait(&checked[quarter][(i - 1) & 1], ((i - 1) >> 1) & 1, err, &stop);
+          ok = warp_wait(&checked[quarter][(i - 1) % kSets], ((i - 1) / kSets) & 1, err, &stop);
           if (!ok) break;
           ref = s_ref[row];
         }
         // (a NaN bound takes the exact path too)
         if (__any_sync(0xffffffffu, !(bound <= ref + kLazy))) {
           mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[32];
+            load(c, v);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 k4 = kn[8 * c + e / 4];
-              const float2 x = mul2(make_float2(f(v[c][e]), f(v[c][e + 1])), make_float2(k4.x, k4.y));
-              const float2 y = mul2(make_float2(f(v[c][e + 2]), f(v[c][e + 3])), make_float2(k4.z, k4.w));
+              const float2 x = mul2(make_float2(f(v[e]), f(v[e + 1])), make_float2(k4.x, k4.y));
+              const float2 y = mul2(make_float2(f(v[e + 2]), f(v[e + 3])), make_float2(k4.z, k4.w));
               mx = max3(mx, x.x, x.y);
               mx = max3(mx, y.x, y.y);
             }
+          }
           mx *= fq;
           if (i == 0) {
             ref = fmaxf(mx, -3.0e38f);
@@ -314,20 +327,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&checked[quarter][i & 1]));
+        if (lane == 0) mbar_arrive(smem_u32(&checked[quarter][w]));
         if (i == w) mine = ref;  // this set's first half: its sum is empty
         l *= fast_exp2(mine - ref);
         mine = ref;
         const float2 f2 = make_float2(fq, fq), r2 = make_float2(-ref, -ref);
         float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          uint32_t p[16];
+          uint32_t v[32], p[16];
+          load(c, v);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 k4 = kn[8 * c + e / 4];
-            const float2 x = fma2(mul2(make_float2(f(v[c][e]), f(v[c][e + 1])), make_float2(k4.x, k4.y)), f2, r2);
-            const float2 y = fma2(mul2(make_float2(f(v[c][e + 2]), f(v[c][e + 3])), make_float2(k4.z, k4.w)), f2, r2);
+            const float2 x = fma2(mul2(make_float2(f(v[e]), f(v[e + 1])), make_float2(k4.x, k4.y)), f2, r2);
+            const float2 y = fma2(mul2(make_float2(f(v[e + 2]), f(v[e + 3])), make_float2(k4.z, k4.w)), f2, r2);
             const float2 px = make_float2(fast_exp2(x.x), fast_exp2(x.y));
             const float2 py = make_float2(fast_exp2(y.x), fast_exp2(y.y));
             sum = add2(sum, add2(px, py));
@@ -349,69 +363,83 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
     ok = ok && warp_wait(&fin, 0, err, &stop);
     s_l[w][row] = l;
     s_lref[w][row] = mine;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
+    // O leaves in the V fragment order, through shared memory (every MMA has
+    // completed and the copies are consumed: the operands' place is free)
+    float *so = reinterpret_cast<float *>(sm);  // [128][kPad]
+    constexpr int kPad = D + 1;
     if (ok && !idle) {
       tc_fence_after();
-      const bool used = row < rows;
-      const long out_row = (long)(u.first + row / per) * a.n_q_heads + h * per + row % per;
-      float *dst = a.partials + (out_row * a.n_slots + split) * (D + 4);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t o[16];
-        tmem_ld16w(tmem + kColO + lanes + 64 * w + 16 * c, o);
+        tmem_ld16w(tmem + kColO + lanes + 32 * w + 16 * c, o);
         ld_wait();
         pin16(o);
-        if (used) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            reinterpret_cast<float4 *>(dst + 4 + 64 * w + 16 * c)[e] =
-                make_float4(f(o[4 * e]) * (1.f / kVScale), f(o[4 * e + 1]) * (1.f / kVScale),
-                            f(o[4 * e + 2]) * (1.f / kVScale), f(o[4 * e + 3]) * (1.f / kVScale));
-        }
+        for (int e = 0; e < 16; ++e)
+          so[row * kPad + a.p.kvperm[32 * w + 16 * c + e]] = f(o[e]) * (1.f / kVScale);
       }
-      if (used && w == 0) {
-        const float ref = s_ref[row];
-        dst[0] = ref;
-        dst[1] = s_l[0][row] * fast_exp2(s_lref[0][row] - ref) +
-                 (n_half > 1 ? s_l[1][row] * fast_exp2(s_lref[1][row] - ref) : 0.f);
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
+    if (ok) {
+      for (int i = warp; i < rows; i += kSoftWarps) {  // a warp per row
+        const long out_row = (long)(u.first + i / per) * a.n_q_heads + h * per + i % per;
+        float *dst = a.partials + (out_row * a.n_slots + split) * (D + 4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) dst[4 + 32 * c + lane] = so[i * kPad + 32 * c + lane];
+        if (lane == 0) {
+          const float ref = s_ref[i];
+          dst[0] = ref;
+          float l_all = 0.f;
+          for (int e = 0; e < min(kSets, n_half); ++e) l_all = fmaf(s_l[e][i], fast_exp2(s_lref[e][i] - ref), l_all);
+          dst[1] = l_all;
+        }
       }
     }
   } else if (warp < kProdWarp) {
-    // ---------------- expansion
-    const int ew = warp - kExpWarp0, r = lane >> 2, q = lane & 3;  // keys 16 ew .. 16 ew + 15 of every tile
+    // ---------------- expansion: keys 16 ew .. 16 ew + 15 of every tile, K~ one
+    // tile ahead of V~ (the scores of a tile are needed that much sooner)
+    const int ew = warp - kExpWarp0, r = lane >> 2, q = lane & 3;
     const Lut lk = fp16_lut<BK>(a.p.cb), lv = fp16_lut<BV>(a.p.cb + 2 * kMaxLevels, kVScale);
     bool ok = true;
-    for (int j = 0; ok && j < n_tiles; ++j) {
-      const int slot = j % kStagesTc, b = j & 1;
-      ok = warp_wait(&full[slot], (j / kStagesTc) & 1, err, &stop);
-      // the q rotation's operands: lo in K~ 0 (fp32 q), hi and Pi in the buffers of tile 1
-      if (ok && ((j == 0 && f32) || j == 1)) ok = warp_wait(&q_mma, 0, err, &stop);
-      if (ok && j >= 2) ok = warp_wait(&k_empty[b], ((j >> 1) - 1) & 1, err, &stop);
-      if (!ok || *(volatile int *)&stop) break;
-      const unsigned char *st = sm + L::ring + slot * L::stage;
-      const int left = t1 - t0 - j * kTcKeys;  // keys of this tile in the split
-      {
+    for (int j = 0; ok && j <= n_tiles; ++j) {
+      if (j < n_tiles) {
+        const int b = j & 1;
+        ok = warp_wait(&full[j % kStagesTc], (j / kStagesTc) & 1, err, &stop);
+        // the q rotation's operands: lo in K~ 0 (fp32 q), hi and Pi in the buffers of tile 1
+        if (ok && ((j == 0 && f32) || j == 1)) ok = warp_wait(&q_mma, 0, err, &stop);
+        if (ok && j >= 2) ok = warp_wait(&k_empty[b], ((j >> 1) - 1) & 1, err, &stop);
+        if (!ok || *(volatile int *)&stop) break;
+        const unsigned char *st = sm + L::ring + (j % kStagesTc) * L::stage;
         // the key norms; past the split's end 1, so that a masked score stays -inf
         const int key = 16 * ew + (lane & 15);
         float n = __half2float(reinterpret_cast<const __half *>(st + St::kn)[key]);
-        if (key >= left) n = 1.f;
+        if (key >= t1 - t0 - j * kTcKeys) n = 1.f;
         if (lane < 16) reinterpret_cast<float *>(sm + L::norms)[(j % kNormBufs) * kTcKeys + key] = n;
+        expand_rows16<BK>(st + St::kc, sm + L::kt + b * kOpBytes, lk, 16 * ew, r, q);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&k_full[b]));
 #pragma unroll
         for (int o = 8; o; o >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
         if (lane == 0) s_kmax[j % kNormBufs][ew] = n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&n_full[j % kNormBufs]));
       }
-      expand_keys16<BK, BV>(st, sm + L::kt + b * kOpBytes, lk, 16 * ew, r, q);
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&k_full[b]));
-      if (j >= 2) ok = warp_wait(&v_empty[b], ((j >> 1) - 1) & 1, err, &stop);
-      if (!ok) break;
-      expand_values16<BK, BV, true>(st, sm + L::vt + b * kOpBytes, lv, 16 * ew, r, q, left);
-      fence_async();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&v_full[b]));
-        mbar_arrive(smem_u32(&empty[slot]));
+      if (j >= 1) {
+        const int t = j - 1, b = t & 1;
+        if (t >= 2) ok = warp_wait(&v_empty[b], ((t >> 1) - 1) & 1, err, &stop);
+        if (!ok) break;
+        const unsigned char *st = sm + L::ring + (t % kStagesTc) * L::stage;
+        expand_rows16<BV, true>(st + St::vc, sm + L::vt + b * kOpBytes, lv, 16 * ew, r, q,
+                                reinterpret_cast<const __half *>(st + St::vn), t1 - t0 - t * kTcKeys);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&v_full[b]));
+          mbar_arrive(smem_u32(&empty[t % kStagesTc]));
+        }
       }
     }
   } else {
@@ -481,10 +509,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t v = sw128_desc(smem_u32(sm + L::vt + (t & 1) * kOpBytes + (i & 1) * kOpBox));
+            const uint64_t v = mn_desc(smem_u32(sm + L::vt + (t & 1) * kOpBytes + (i & 1) * (kHalf * 128)), kOpBox);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // (16 keys: 32 bytes, 2 descriptor units)
-              mma_ts(tmem + kColO, tmem + kColS + kHalf * buf + 8 * kk, v + 2 * kk, kDescO, (i > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)  // (16 keys: 2048 bytes)
+              mma_ts(tmem + kColO, tmem + kColS + kHalf * buf + 8 * kk, v + kk * (2048 >> 4), kDescO,
+                     (i > 0 || kk > 0) ? 1u : 0u);
             tc_commit(smem_u32(&pv_done[buf]));
             if ((i & 1) || i + 1 == n_half) tc_commit(smem_u32(&v_empty[t & 1]));
           }
@@ -501,8 +530,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
               const uint32_t off = ((kk >> 2) * kOpBox + (kk & 3) * 32) >> 4;
-              mma_ts(d, tmem + kColQ + 8 * kk, k + off, kDescO, kk > 0);
-              mma_ts(d, tmem + kColQ + 64 + 8 * kk, k + off, kDescO, 1);
+              mma_ts(d, tmem + kColQ + 8 * kk, k + off, kDescS, kk > 0);
+              mma_ts(d, tmem + kColQ + 64 + 8 * kk, k + off, kDescS, 1);
             }
             tc_commit(smem_u32(&s_full[n & 1]));
             tc_commit(smem_u32(&k_empty[n & 1]));

@@ -19,6 +19,14 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// MN-major shared-memory descriptor (values stored token by token):
+// 128-byte swizzle, 64-column blocks `block` bytes apart, groups of eight
+// tokens 1024 bytes apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t block) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
 // One lane of a converged warp.  MMAs are issued by a whole warp that runs the
 // same code with `if (elect_one())` around them: operands that are the same in
 // every lane then live in uniform registers.  (Under `if (lane == 0)` each

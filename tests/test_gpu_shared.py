@@ -138,7 +138,7 @@ class Batch:
                                    ints(self.prefixes), mg, mp, ms, out, lse, workspace, scale=scale, stream=stream)
         return out, lse
 
-    def check(self, out, lse, scale=None, skip=(), large=False):
+    def check(self, out, lse, scale=None, skip=(), large=False, heads_of=None):
         p = params(self.d, self.bits_k, self.bits_v, self.qjl)
         f16 = ph.f16_bits_to_f64
         bf16 = out.dtype == torch.bfloat16
@@ -152,7 +152,7 @@ class Batch:
                 continue
             g = self.group_of[s]
             lead, pre = self.groups[g], self.prefixes[g]
-            for h in range(self.n_kv):
+            for h in heads_of or range(self.n_kv):
                 cat = lambda name: np.concatenate([self.rows(name, lead, h, 0, pre), self.rows(name, s, h, pre, n)])  # noqa: E731
                 heads = slice(h * self.per, (h + 1) * self.per)
                 extra = {}
@@ -242,6 +242,22 @@ def test_large_norms(tq):
 def test_long_prefix_over_many_splits(tq, n, per):
     rng = np.random.default_rng(n)
     Batch(tq, [0, n], [20001], (20001 + rng.integers(0, 700, n)).tolist(), n_kv=1, per=per, seed=3).run()
+
+
+@pytest.mark.parametrize("prefix", [1400, 2049])
+@pytest.mark.parametrize("bits_k,bits_v", [(3, 3), (4, 2)])
+def test_many_key_tiles_in_one_split(tq, prefix, bits_k, bits_v):
+    """As many (group, KV head) pairs as the GPU has SMs, so that every CTA walks its prefix alone; keys whose
+    scores rise along the prefix, so that a row's maximum keeps moving."""
+    groups = [5 * g for g in range(11)]
+    b = Batch(tq, groups, [prefix] * 10, [prefix + 3 * (s % 7) for s in range(50)], n_kv=16, per=4, bits_k=bits_k,
+              bits_v=bits_v, seed=prefix)
+    up = (np.linspace(1, 40, b.cap)[None, None, :] * np.ones(b.planes["norm_k"].shape)).astype(np.float16)
+    b.planes["norm_k"] = b._poison(up.view(np.int16))
+    b.cache.planes["norm_k"].copy_(torch.from_numpy(b.planes["norm_k"]))
+    out, lse = b.call()
+    b.ctx.check_device_errors()
+    b.check(out, lse, skip=[s for s in range(50) if s % 9], heads_of=(0, 15))
 
 
 def test_many_groups(tq):
