@@ -581,8 +581,8 @@ tq_status check_shared_sizes(const tq_cache *cache, int32_t n_q_heads, int32_t n
                 cache->n_kv_heads);
   if (n_q_heads / cache->n_kv_heads > 16)
     return fail(TQ_ERR_UNSUPPORTED, "query heads per KV head = %d > 16", n_q_heads / cache->n_kv_heads);
-  if (cache->n_seqs > 65535 || cache->n_kv_heads > 65535)
-    return fail(TQ_ERR_UNSUPPORTED, "n_seqs=%d n_kv_heads=%d: at most 65535", cache->n_seqs, cache->n_kv_heads);
+  if (cache->n_seqs >= 65535 || cache->n_kv_heads > 65535)
+    return fail(TQ_ERR_UNSUPPORTED, "n_seqs=%d n_kv_heads=%d: at most 65534 and 65535", cache->n_seqs, cache->n_kv_heads);
   if ((int64_t)cache->n_seqs * n_q_heads > INT32_MAX)
     return fail(TQ_ERR_UNSUPPORTED, "n_seqs * n_q_heads = %lld does not fit 31 bits",
                 (long long)cache->n_seqs * n_q_heads);

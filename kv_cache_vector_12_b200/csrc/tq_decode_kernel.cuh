@@ -66,6 +66,9 @@ struct DecodeArgs {
   int pass;                          // kPassPrefix or kPassSuffix
   int members;                       // sequences per CTA of the prefix pass
   int slot0;                         // first partial slot of this pass (n_splits counts both passes' slots)
+  // the pass behind the prefixes runs beside the prefix pass, launched before
+  // it: only CTA (0, 0, n_seqs), which has no other work, waits for that grid
+  bool beside;
 };
 
 enum SharedPass { kPassPrefix = 0, kPassSuffix = 1 };
@@ -301,7 +304,18 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
   __syncthreads();
   // launched as a programmatic dependent: the cache, q and seq_lens are final
   // once the previous kernel in the stream has completed
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (SHARED) {
+    // Every CTA of the prefix pass lets the next grid start as soon as the
+    // kernels in front of the call have completed, so that grid may read
+    // whatever they wrote without waiting; the merge behind it waits for it,
+    // and so through its last CTA for the prefix pass.
+    const bool last = a.beside && (int)blockIdx.z == a.c.n_seqs;
+    if (last ? blockIdx.x + blockIdx.y == 0 : !a.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (last) return;
+    if (a.pass == kPassPrefix) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   int t_first = 0, t_low = 0, t_end = 0;  // SHARED: first position copied, first attended, end
   if constexpr (SHARED) {
     SharedUnit u;

@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kTcMinRows = 16;   // rows of a group above which the tcgen05 prefix pass runs
 constexpr int kTcFixed = 4;
-constexpr int kMaxSlots = 1024;  // split partials of one row, both passes
+constexpr int kSuffixFixed = 1;
 
 struct MergeArgs {
   DeviceParams p;
@@ -38,68 +38,80 @@ struct MergeArgs {
   float *lse;
 };
 
-// One CTA of 128 threads per (sequence, query head).
+// kMergeRows (sequence, query head) rows per CTA of 128 threads: a warp joins
+// the split partials of one row, then every thread takes output coordinate
+// `tid` (and tid + 128 at d = 256) of all of them, so that a row of Pi^T is
+// loaded once for kMergeRows rows.  One row per CTA, as the merge of
+// tq_decode_attention has it, read Pi^T (32 KB) for every row: 21 us for 1024
+// rows of 25 partials where this takes 11.
+constexpr int kMergeRows = 4;
+
 template <int DH>
-__global__ void __launch_bounds__(128) shared_merge_kernel(const MergeArgs a) {
+__global__ void __launch_bounds__(128) shared_merge_kernel(const MergeArgs a, int n_rows) {
   constexpr int PF = DH + 4, PL = DH / 32;
-  __shared__ float s_ot[DH];
-  __shared__ float s_w[kMaxSlots];
-  __shared__ __align__(16) float s_acc[4][DH];
-  __shared__ float red[4];
-  const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ __align__(16) float s_ot[kMergeRows][DH];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row0 = blockIdx.x * kMergeRows, row = row0 + warp;
   Bf16Row<DH> pw0, pw1;
   if (tid < DH) pw0.load(a.p.pivt + tid * DH);
   if constexpr (DH == 256) pw1.load(a.p.pivt + (tid + 128) * DH);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int s = row / a.n_q_heads;
-  const SeqRange g = sequence_range(a.cu_group, a.prefix, a.n_groups, a.seq_lens, a.max_group, a.max_prefix,
-                                    a.max_suffix, a.capacity, s, lane);
-  // the slots in use: the splits that hold positions, of either pass
-  const int n_p = g.len > 0 && a.p_splits ? (g.prefix + a.p_chunk - 1) / a.p_chunk : 0;
-  const int n_s = g.len > g.prefix ? (g.len - (g.prefix & ~63) + a.s_chunk - 1) / a.s_chunk : 0;
-  const int used = n_p + n_s;
-  const float *src = a.partials + (long)row * (a.p_splits + a.s_splits) * PF;
-  auto slot = [&](int i) { return src + (long)(i < n_p ? i : a.p_splits + i - n_p) * PF; };
-  float mloc = -INFINITY;
-  for (int i = tid; i < used; i += 128) mloc = fmaxf(mloc, s_w[i] = slot(i)[0]);
-  const float mm = block_max128(mloc, red);
-  float lpart = 0.f;
-  for (int i = tid; i < used; i += 128) {
-    const float w = s_w[i] == -INFINITY ? 0.f : exp2f(s_w[i] - mm);
-    s_w[i] = w;
-    lpart = fmaf(w, slot(i)[1], lpart);
+  if (row < n_rows) {
+    const int s = row / a.n_q_heads;
+    const SeqRange g = sequence_range(a.cu_group, a.prefix, a.n_groups, a.seq_lens, a.max_group, a.max_prefix,
+                                      a.max_suffix, a.capacity, s, lane);
+    // the slots in use: the splits that hold positions, of either pass
+    const int n_p = g.len > 0 && a.p_splits ? (g.prefix + a.p_chunk - 1) / a.p_chunk : 0;
+    const int n_s = g.len > g.prefix ? (g.len - (g.prefix & ~63) + a.s_chunk - 1) / a.s_chunk : 0;
+    const int used = n_p + n_s;
+    const float *src = a.partials + (long)row * (a.p_splits + a.s_splits) * PF;
+    auto slot = [&](int i) { return src + (long)(i < n_p ? i : a.p_splits + i - n_p) * PF; };
+    float mm = -INFINITY, ll = 0.f, acc[PL];
+#pragma unroll
+    for (int c = 0; c < PL; ++c) acc[c] = 0.f;
+    for (int i0 = 0; i0 < used; i0 += 32) {  // 32 slots at a time: lane i holds (m, l) of slot i0 + i
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < used) ml = *reinterpret_cast<const float2 *>(slot(i0 + lane));
+      float mx = ml.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float nm = fmaxf(mm, mx), old = mm == -INFINITY ? 0.f : exp2f(mm - nm);
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - nm);
+      mm = nm;
+      float lw = w * ml.y;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+      ll = fmaf(ll, old, lw);
+#pragma unroll
+      for (int c = 0; c < PL; ++c) acc[c] *= old;
+      const int n = min(32, used - i0);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        float v[PL];
+        load_floats<PL>(slot(i0 + i) + 4 + lane * PL, v);
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+        for (int c = 0; c < PL; ++c) acc[c] = fmaf(wi, v[c], acc[c]);
+      }
+    }
+    const float il = used > 0 ? 1.f / ll : 0.f;
+#pragma unroll
+    for (int c = 0; c < PL; ++c) s_ot[warp][lane * PL + c] = acc[c] * il;
+    if (a.lse && lane == 0) a.lse[row] = used > 0 ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
   }
   __syncthreads();
-  float acc[PL];
-#pragma unroll
-  for (int c = 0; c < PL; ++c) acc[c] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < used; i += 4) {
-    float v[PL];
-    load_floats<PL>(slot(i) + 4 + lane * PL, v);
-    const float w = s_w[i];
-#pragma unroll
-    for (int c = 0; c < PL; ++c) acc[c] = fmaf(w, v[c], acc[c]);
-  }
-#pragma unroll
-  for (int c = 0; c < PL; ++c) s_acc[warp][lane * PL + c] = acc[c];
-  for (int o = 16; o; o >>= 1) lpart += __shfl_xor_sync(0xffffffffu, lpart, o);
-  if (lane == 0) red[warp] = lpart;
-  __syncthreads();
-  const float ll = (red[0] + red[1]) + (red[2] + red[3]);
-  for (int i = tid; i < DH; i += 128) {
-    const float oo = (s_acc[0][i] + s_acc[1][i]) + (s_acc[2][i] + s_acc[3][i]);
-    s_ot[i] = used > 0 ? oo / ll : 0.f;
-  }
-  __syncthreads();
-  auto store = [&](int i, float x) {
-    if (a.out_f32) static_cast<float *>(a.out)[(long)row * DH + i] = x;
-    else static_cast<__nv_bfloat16 *>(a.out)[(long)row * DH + i] = __float2bfloat16_rn(x);
+  auto store = [&](int e, int i, float x) {
+    const long at = (long)(row0 + e) * DH + i;
+    if (a.out_f32) static_cast<float *>(a.out)[at] = x;
+    else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(x);
   };
-  if (tid < DH) store(tid, dot_bf16_row<DH>(pw0, s_ot));
-  if constexpr (DH == 256) store(tid + 128, dot_bf16_row<DH>(pw1, s_ot));
-  if (a.lse && tid == 0) a.lse[row] = used > 0 ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+  for (int e = 0; e < kMergeRows; ++e) {
+    if (row0 + e >= n_rows) break;
+    if (tid < DH) store(e, tid, dot_bf16_row<DH>(pw0, s_ot[e]));
+    if constexpr (DH == 256) store(e, tid + 128, dot_bf16_row<DH>(pw1, s_ot[e]));
+  }
 }
 
 }  // namespace
@@ -136,11 +148,25 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
     s.p_splits = sp.n_splits;
   }
   s.nt_s = per > 8 ? 2 : 1;
-  // (the suffix pass starts up to 63 positions before the prefix's end)
-  const DecodeSplit ss =
-      decode_split(n_seqs, n_kv_heads, max_suffix + 63, shared_ctas_per_sm(d, bits_k, bits_v, qjl, s.nt_s));
-  s.s_chunk = ss.chunk;
-  s.s_splits = ss.n_splits;
+  // The pass behind the prefix starts up to 63 positions before the prefix's
+  // end.  Its units are many and short, so a split has to pay for its CTA's
+  // prologue (about kSuffixFixed stages of 128 positions): the count with the
+  // fewest stage times over all waves.  32 sequences of up to 1500 positions
+  // behind their prefix, 8 KV heads: 7 splits 30 us, 2 splits 20.
+  {
+    const long stages = (max_suffix + 63 + 127) / 128, units = (long)n_seqs * n_kv_heads;
+    const long slots = (long)sm_count() * shared_ctas_per_sm(d, bits_k, bits_v, qjl, s.nt_s);
+    long best = -1;
+    for (long n = 1; n <= stages && n <= 64; ++n) {
+      const long per_split = (stages + n - 1) / n, used = (stages + per_split - 1) / per_split;
+      const long cost = (units * used + slots - 1) / slots * (per_split + kSuffixFixed);
+      if (best < 0 || cost < best) {
+        best = cost;
+        s.s_chunk = (int)(per_split * 128);
+        s.s_splits = (int)used;
+      }
+    }
+  }
   const size_t rows = (size_t)n_seqs * n_q_heads;
   s.workspace = (rows * (size_t)(s.p_splits + s.s_splits) * (size_t)(d + 4) * sizeof(float) + 255) / 256 * 256;
   return s;
@@ -200,7 +226,8 @@ int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q
     args.pass = kPassSuffix;
     args.chunk = plan.s_chunk;
     args.slot0 = plan.p_splits;
-    cfg.gridDim = dim3(plan.s_splits, c.n_kv_heads, c.n_seqs);
+    args.beside = plan.p_splits > 0;
+    cfg.gridDim = dim3(plan.s_splits, c.n_kv_heads, c.n_seqs + (args.beside ? 1 : 0));
     cfg.dynamicSmemBytes = v.smem;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, v.fn, args);
     if (e != cudaSuccess) return (int)e;
@@ -208,11 +235,12 @@ int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q
   const MergeArgs m{p,          seq_lens,   cu_group,  prefix,       n_groups,      max_group,    max_prefix,
                     max_suffix, c.capacity, n_q_heads, plan.p_chunk, plan.p_splits, plan.s_chunk, plan.s_splits,
                     args.partials, out, out_f32, lse};
-  cfg.gridDim = dim3((unsigned)(c.n_seqs * n_q_heads));
+  const int n_rows = c.n_seqs * n_q_heads;
+  cfg.gridDim = dim3((unsigned)((n_rows + kMergeRows - 1) / kMergeRows));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   const auto merge = p.d == 64 ? shared_merge_kernel<64> : p.d == 256 ? shared_merge_kernel<256> : shared_merge_kernel<128>;
-  return (int)cudaLaunchKernelEx(&cfg, merge, m);
+  return (int)cudaLaunchKernelEx(&cfg, merge, m, n_rows);
 }
 
 }  // namespace tq

