@@ -7,9 +7,9 @@
 //   l_i = sum_{j <= i} p_ij,            c = scale log2(e),
 //   lse_i = ln 2 (r_i + log2 l_i)
 // with r_i a running reference: the row's maximum when it was last moved.
-// Keys are taken in tiles; r_i moves only when a tile's maximum passes it by
-// more than kLazy (so p <= 2^kLazy, far below the range of bf16 and fp32),
-// which makes rescaling O rare: after the first tiles almost no row moves.
+// Keys are taken 64 at a time; r_i moves only when a step's maximum passes it
+// by more than kLazy (so p <= 2^kLazy, far below the range of bf16 and fp32),
+// which makes rescaling O rare: after the first steps almost no row moves.
 //
 // A CTA takes NT tiles of 128 query rows of one KV head (a row is one
 // (position, query head) pair: with G heads per KV head a tile holds 128 / G
@@ -17,15 +17,18 @@
 // token still fills G rows) against the keys at or before them:
 //   producer  (1 thread)  Q once, then K and V tiles by TMA into a ring of
 //             128-byte-swizzled slots;
-//   MMA       (1 thread)  S = Q K^T, then O += P V with P as the A operand in
+//   MMA       (1 warp per row tile)  S = Q K^T, then O += P V with P as the A operand in
 //             tensor memory and V read from its token-major tile as an
 //             MN-major B operand (no transpose anywhere);
 //   softmax   (4 warps per row tile, one thread per row)  S from tensor
-//             memory, mask on diagonal tiles only, exp2, P as bf16 back into
-//             tensor memory, and at the end O / l to global memory.
-// With two row tiles (d = 64 and 128) the MMAs of one run under the softmax
-// of the other; at d = 256 one row tile fills tensor memory and S is
-// double-buffered over tiles of 64 keys instead.
+//             memory, mask on diagonal steps only, exp2, P as bf16 back over
+//             the S it came from, and at the end O / l to global memory.
+// Every row tile has two S buffers of 64 keys: the scores of step h + 1 are
+// there when the softmax of step h ends, so the softmax warps, which bound the
+// kernel (one exp2 per score), do not wait for an MMA.  (With one buffer of
+// 128 keys a row tile alternated between 2000 cycles of softmax and 2100 of
+// hand-over and MMAs.)  Two row tiles per CTA at d = 64 and 128, one at d = 256,
+// where O alone takes half of tensor memory.
 // P is rounded to bf16, V's type (one MMA takes one type for A and B); l is
 // summed in fp32 from the unrounded weights.
 #include <cuda_bf16.h>
@@ -38,12 +41,14 @@
 namespace tq {
 namespace {
 
+constexpr int kStep = 64;     // keys per step: one S buffer
 constexpr float kLazy = 8.f;  // log2 units a tile's maximum may pass the reference
 
 template <int DH>
 struct PromptCfg {
   static constexpr int NT = DH == 256 ? 1 : 2;      // row tiles of 128
-  static constexpr int KT = DH == 256 ? 64 : 128;   // keys per tile
+  static constexpr int KT = DH == 256 ? 64 : 128;   // keys per tile of K or V
+  static constexpr int kSteps = KT / kStep;         // steps per tile
   static constexpr int kBoxes = DH / 64;            // 64-column swizzled boxes per operand
   static constexpr int kQBox = 128 * 128;           // bytes of one box of a Q tile
   static constexpr int kKVBox = KT * 128;           // bytes of one box of a K or V tile
@@ -52,16 +57,15 @@ struct PromptCfg {
   static constexpr int kSlots = DH == 64 ? 8 : 5;
   static constexpr int kSoftWarps = 4 * NT;
   static constexpr int kProdWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-  static constexpr int kThreads = 32 * (kSoftWarps + 2);
+  static constexpr int kThreads = 32 * (kSoftWarps + 1 + NT);  // an MMA warp per row tile
   static constexpr int smem = 1024 + NT * kQTile + kSlots * kSlot;
-  // tensor-memory columns: S (P overwrites it when NT == 2) and O
-  static constexpr uint32_t s_col(int i) { return NT == 2 ? 128u * i : 256u + 64u * i; }
-  static constexpr uint32_t p_col(int i) { return NT == 2 ? 128u * i : 384u + 32u * i; }
-  static constexpr uint32_t o_col(int i) { return NT == 2 ? 256u + (uint32_t)DH * i : 0u; }
+  // tensor-memory columns: two S buffers per row tile (P over them) and O
+  static constexpr uint32_t s_col(int i, int b) { return 128u * i + 64u * b; }
+  static constexpr uint32_t o_col(int i) { return 128u * NT + (uint32_t)DH * i; }
   // instruction descriptors, kind::f16: bf16 A and B, fp32 D, M = 128; S has
   // both operands K-major, O has B MN-major (bit 16)
   static constexpr uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
-  static constexpr uint32_t idesc_s = base | ((uint32_t)(KT >> 3) << 17);
+  static constexpr uint32_t idesc_s = base | ((uint32_t)(kStep >> 3) << 17);
   static constexpr uint32_t idesc_o = base | (1u << 16) | ((uint32_t)(DH >> 3) << 17);
 };
 
@@ -183,11 +187,11 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
   unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   unsigned char *ring = sm + NT * C::kQTile;
   __shared__ __align__(8) uint64_t q_full, full[C::kSlots], empty[C::kSlots];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], fin;
+  __shared__ __align__(8) uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], fin[2];  // [row tile][buffer]
   __shared__ uint32_t tmem_slot;
   __shared__ int stop, s_seq, s_blk;
 
-  const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31, h = blockIdx.y;
+  const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31, h_kv = blockIdx.y;
   const int G = a.n_q_heads / a.n_kv_heads, PC = a.per_tile, span = NT * PC;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {
@@ -207,55 +211,62 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
     bar_init(smem_addr(&q_full), 1);
     for (int i = 0; i < C::kSlots; ++i) {
       bar_init(smem_addr(&full[i]), 1);
-      bar_init(smem_addr(&empty[i]), 1);
+      bar_init(smem_addr(&empty[i]), NT);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(smem_addr(&s_full[i]), 1);
-      bar_init(smem_addr(&p_full[i]), 128);
+      for (int b = 0; b < 2; ++b) {
+        bar_init(smem_addr(&s_full[i][b]), 1);
+        bar_init(smem_addr(&p_full[i][b]), 4);
+      }
+      bar_init(smem_addr(&pv_done[i]), 1);
       bar_init(smem_addr(&o_full[i]), 1);
+      bar_init(smem_addr(&fin[i]), 1);
     }
-    bar_init(smem_addr(&fin), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // all 512 columns are this CTA's: the base is column 0 of lane 0
-  constexpr uint32_t tmem = 0;
+  // (all 512 columns are this CTA's: addresses start at column 0 of lane 0)
   const int s = s_seq;
 
   if (s >= 0) {
     const int tok0 = a.cu[s], len = a.cu[s + 1] - tok0;
     const int first = s_blk * span;                    // first query position
-    // keys at or before the last query of each row tile, and their tiles
-    int tiles[2] = {0, 0};
+    // keys at or before the last query of each row tile, in steps and tiles
+    int steps[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int b = first + i * PC, e = min(len, b + PC);
-      tiles[i] = e > b ? (e + KT - 1) / KT : 0;
+      steps[i] = e > b ? (e + kStep - 1) / kStep : 0;
     }
-    const int n_tiles = NT == 2 ? max(tiles[0], tiles[1]) : tiles[0];
+    const int n_steps = NT == 2 ? max(steps[0], steps[1]) : steps[0];
+    const int n_tiles = (n_steps + C::kSteps - 1) / C::kSteps;
 
     if (warp == C::kProdWarp) {
       // ---------------- producer
       if (lane == 0) {
         const uint32_t box = (uint32_t)(PC * G * 128);
-        bar_expect_tx(smem_addr(&q_full), (NT == 2 && tiles[1] ? 2 : 1) * C::kBoxes * box);
+        bar_expect_tx(smem_addr(&q_full), (NT == 2 && steps[1] ? 2 : 1) * C::kBoxes * box);
         for (int i = 0; i < NT; ++i)
-          if (tiles[i])
+          if (steps[i])
             for (int b = 0; b < C::kBoxes; ++b)
-              tma_load_3d(smem_addr(sm + i * C::kQTile + b * C::kQBox), &map_q, 64 * b, h * G, tok0 + first + i * PC,
+              tma_load_3d(smem_addr(sm + i * C::kQTile + b * C::kQBox), &map_q, 64 * b, h_kv * G, tok0 + first + i * PC,
                           smem_addr(&q_full));
         int issued = 0;
+        int slot = 0, phase = 1;
         for (int it = 0; it < 2 * n_tiles; ++it) {  // K 0, V 0, K 1, V 1, ...
-          const int slot = it % C::kSlots, use = it / C::kSlots;
-          if (use > 0 && !wait_or_stop(&empty[slot], (use - 1) & 1, a.err, &stop)) break;
+          if (it >= C::kSlots && !wait_or_stop(&empty[slot], phase, a.err, &stop)) break;
           if (*(volatile int *)&stop) break;
           bar_expect_tx(smem_addr(&full[slot]), C::kSlot);
           for (int b = 0; b < C::kBoxes; ++b)
-            tma_load_3d(smem_addr(ring + slot * C::kSlot + b * C::kKVBox), (it & 1) ? &map_v : &map_k, 64 * b, h,
+            tma_load_3d(smem_addr(ring + slot * C::kSlot + b * C::kKVBox), (it & 1) ? &map_v : &map_k, 64 * b, h_kv,
                         tok0 + (it >> 1) * KT, smem_addr(&full[slot]));
           issued = it + 1;
+          if (++slot == C::kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
         if (*(volatile int *)&stop) {  // never leave copies in flight
           bar_wait(smem_addr(&q_full), 0);
@@ -263,169 +274,135 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
             bar_wait(smem_addr(&full[it % C::kSlots]), (it / C::kSlots) & 1);
         }
       }
-    } else if (warp == C::kMmaWarp) {
-      // ---------------- MMA issuer (the whole warp; one lane issues)
-      auto slot_desc = [&](int it) { return smem_addr(ring + (it % C::kSlots) * C::kSlot); };
-      auto loaded = [&](int it) { return warp_wait(&full[it % C::kSlots], (it / C::kSlots) & 1, a.err, &stop); };
-      auto scores = [&](int i, int buf, int j) {  // row tile i, tensor-memory buffer buf, key tile j
-        const uint64_t q = sw128_desc(smem_addr(sm + i * C::kQTile)), k = sw128_desc(slot_desc(2 * j));
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk)
-          tc_mma_n(tmem + C::s_col(buf), q + (((kk >> 2) * C::kQBox + (kk & 3) * 32) >> 4),
-                   k + (((kk >> 2) * C::kKVBox + (kk & 3) * 32) >> 4), C::idesc_s, kk > 0);
+    } else if (warp >= C::kMmaWarp) {
+      // ---------------- MMA issuer of row tile i (the whole warp; one lane
+      // issues).  A warp per row tile: with one for both, the issue (about 55
+      // cycles an MMA beside busy softmax warps) and the waits in between took
+      // longer than the MMAs.
+      const int i = warp - C::kMmaWarp, mine = steps[i];
+      // K tile of the step whose scores are next and V tile of the step whose
+      // values are next: ring slots and their phases, advanced without division
+      int ks = 0, kp = 0, vs = 1, vp = 0;
+      auto advance = [&](int &slot, int &phase) {
+        slot += 2;
+        if (slot >= C::kSlots) {
+          slot -= C::kSlots;
+          phase ^= 1;
+        }
       };
-      auto values = [&](int i, int buf, int j) {
-        const uint64_t v = mn_desc(slot_desc(2 * j + 1), C::kKVBox);
-#pragma unroll
-        for (int kk = 0; kk < KT / 16; ++kk)  // 16 tokens: 2048 bytes
-          mma_ts(tmem + C::o_col(i), tmem + C::p_col(buf) + 8 * kk, v + kk * (2048 >> 4), C::idesc_o,
-                 (j > 0 || kk > 0) ? 1u : 0u);
-      };
-      bool ok = warp_wait(&q_full, 0, a.err, &stop) && loaded(0);
-      if (ok) {
+      const uint64_t q = sw128_desc(smem_addr(sm + i * C::kQTile));
+      const uint64_t k0 = sw128_desc(smem_addr(ring)), v0 = mn_desc(smem_addr(ring), C::kKVBox);
+      const uint32_t d_o = C::o_col(0) + (uint32_t)DH * i, d_s = 128u * i;
+      constexpr int kSlotU = C::kSlot >> 4, kStepU = (kStep * 128) >> 4;  // descriptor units
+      // Step h: O += P V, then S of step h + 2 over the P just read (MMAs of one
+      // thread run in order); two S go ahead.  A tile's slot is given back after
+      // its last step, also by a row tile that needs fewer.
+      bool ok = warp_wait(&q_full, 0, a.err, &stop);
+      const int last = n_tiles * C::kSteps;
+#pragma unroll 1
+      for (int h = -2; ok && h < last; ++h) {
+        const int n = h + 2;
+        if (h >= 0 && h % C::kSteps == 0) ok = warp_wait(&full[vs], vp, a.err, &stop);
+        if (ok && n < last && n % C::kSteps == 0) ok = warp_wait(&full[ks], kp, a.err, &stop);
+        if (ok && h >= 0 && h < mine) ok = warp_wait(&p_full[i][h & 1], (h >> 1) & 1, a.err, &stop);
+        if (!ok || __shfl_sync(0xffffffffu, *(volatile int *)&stop, 0)) break;
         tc_fence_after();
+        const bool v_end = h >= 0 && h % C::kSteps == C::kSteps - 1, k_end = n < last && n % C::kSteps == C::kSteps - 1;
         if (elect_one()) {
+          if (h >= 0 && h < mine) {
+            const uint64_t v = v0 + (uint64_t)(vs * kSlotU + (h % C::kSteps) * kStepU);
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            if (tiles[i] > 0) {
-              scores(i, i, 0);
-              tc_commit(smem_addr(&s_full[i]));
-            }
-          tc_commit(smem_addr(&empty[0]));
+            for (int kk = 0; kk < kStep / 16; ++kk)  // 16 tokens: 2048 bytes
+              mma_ts(d_o, d_s + 64u * (h & 1) + 8 * kk, v + kk * (2048 >> 4), C::idesc_o, (h > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(smem_addr(&pv_done[i]));
+            if (h + 1 == mine) tc_commit(smem_addr(&o_full[i]));
+          }
+          if (v_end) tc_commit(smem_addr(&empty[vs]));
+          if (n < mine) {
+            const uint64_t k = k0 + (uint64_t)(ks * kSlotU + (n % C::kSteps) * kStepU);
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk)
+              tc_mma_n(d_s + 64u * (n & 1), q + (((kk >> 2) * C::kQBox + (kk & 3) * 32) >> 4),
+                       k + (((kk >> 2) * C::kKVBox + (kk & 3) * 32) >> 4), C::idesc_s, kk > 0);
+            tc_commit(smem_addr(&s_full[i][n & 1]));
+          }
+          if (k_end) tc_commit(smem_addr(&empty[ks]));
         }
         __syncwarp();
-      }
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        const bool more = j + 1 < n_tiles;
-        if constexpr (NT == 1) {
-          if (more) {
-            ok = loaded(2 * j + 2);
-            if (!ok || *(volatile int *)&stop) break;
-            // S and P buffer (j + 1) % 2 were last used by tile j - 1, whose
-            // weights were complete before its value MMAs were issued
-            if (elect_one()) {
-              scores(0, (j + 1) & 1, j + 1);
-              tc_commit(smem_addr(&s_full[(j + 1) & 1]));
-              tc_commit(smem_addr(&empty[(2 * j + 2) % C::kSlots]));
-            }
-            __syncwarp();
-          }
-          ok = loaded(2 * j + 1) && warp_wait(&p_full[j & 1], (j >> 1) & 1, a.err, &stop);
-          if (!ok || *(volatile int *)&stop) break;
-          tc_fence_after();
-          if (elect_one()) {
-            values(0, j & 1, j);
-            tc_commit(smem_addr(&o_full[0]));
-            if (!more) tc_commit(smem_addr(&o_full[1]));
-            tc_commit(smem_addr(&empty[(2 * j + 1) % C::kSlots]));
-          }
-          __syncwarp();
-        } else {
-          // O += P V of tile j, then S of tile j + 1 (over the P just read:
-          // MMAs of one thread run in order), for each row tile in turn
-          ok = loaded(2 * j + 1) && (!more || loaded(2 * j + 2));
-          if (!ok || *(volatile int *)&stop) break;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (j >= tiles[i]) continue;
-            ok = ok && warp_wait(&p_full[i], j & 1, a.err, &stop);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              values(i, i, j);
-              if (j + 1 < tiles[i]) {
-                scores(i, i, j + 1);
-                tc_commit(smem_addr(&s_full[i]));
-              } else {
-                tc_commit(smem_addr(&o_full[i]));
-              }
-            }
-            __syncwarp();
-          }
-          if (!ok || *(volatile int *)&stop) break;
-          if (elect_one()) {
-            tc_commit(smem_addr(&empty[(2 * j + 1) % C::kSlots]));
-            if (more) tc_commit(smem_addr(&empty[(2 * j + 2) % C::kSlots]));
-          }
-          __syncwarp();
-        }
+        if (v_end) advance(vs, vp);
+        if (k_end) advance(ks, kp);
       }
       // every MMA issued here has completed before the tensor memory is released
-      if (elect_one()) tc_commit(smem_addr(&fin));
+      if (elect_one()) tc_commit(smem_addr(&fin[i]));
       __syncwarp();
-      bar_wait(smem_addr(&fin), 0);
+      bar_wait(smem_addr(&fin[i]), 0);
     } else {
       // ---------------- softmax: row tile i, one thread per row
       const int i = NT == 2 ? warp >> 2 : 0, row = tid & 127;
-      const int n = tiles[i], base = first + i * PC;
+      const int n = steps[i], base = first + i * PC;
       const int t = row / G, pos = (row < PC * G && base + t < len) ? base + t : -1;
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-      const uint32_t t_o = tmem + C::o_col(i) + lanes;
+      const uint32_t t_o = C::o_col(i) + lanes;
       float ref = 0.f, l = 0.f;
       bool ok = true;
-      for (int j = 0; j < n; ++j) {
-        const int buf = NT == 2 ? i : (j & 1);
-        const uint32_t par = NT == 2 ? (j & 1) : ((j >> 1) & 1);
-        ok = warp_wait(&s_full[buf], par, a.err, &stop);
+#pragma unroll 1
+      for (int h = 0; h < n; ++h) {
+        const uint32_t t_s = C::s_col(i, h & 1) + lanes;
+        ok = warp_wait(&s_full[i][h & 1], (h >> 1) & 1, a.err, &stop);
         if (!ok || *(volatile int *)&stop) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t v[KT / 32][32];
+        uint32_t v[2][32];
 #pragma unroll
-        for (int c = 0; c < KT / 32; ++c) tmem_ld32(tmem + C::s_col(buf) + lanes + 32 * c, v[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld32(t_s + 32 * c, v[c]);
         ld_wait();
 #pragma unroll
-        for (int c = 0; c < KT / 32; ++c) pin32(v[c]);
-        const int key0 = j * KT;
-        if (key0 + KT - 1 > base) {  // some row of the tile does not see every key
+        for (int c = 0; c < 2; ++c) pin32(v[c]);
+        const int key0 = h * kStep;
+        if (key0 + kStep - 1 > base) {  // some row of the tile does not see every key
 #pragma unroll
-          for (int c = 0; c < KT / 32; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (key0 + 32 * c + e > pos) v[c][e] = 0xff800000u;
         }
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < KT / 32; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) mx = max3(mx, f(v[c][e]), f(v[c][e + 1]));
         mx *= a.c;
-        if (j == 0) {
+        if (h == 0) {
           ref = fmaxf(mx, -3.0e38f);
-        } else {
-          // O may be rescaled as soon as the value MMAs of tile j - 1 are done
-          const bool move = mx > ref + kLazy;
-          if (__any_sync(0xffffffffu, move)) {
-            if constexpr (NT == 1) {
-              ok = warp_wait(&o_full[0], (j - 1) & 1, a.err, &stop);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            const float nref = fmaxf(ref, mx), al = ex2(ref - nref);
-            ref = nref;
-            l *= al;
+        } else if (__any_sync(0xffffffffu, mx > ref + kLazy)) {
+          // O is rescaled once the values of step h - 1 are in it
+          ok = warp_wait(&pv_done[i], (h - 1) & 1, a.err, &stop);
+          if (!ok) break;
+          tc_fence_after();
+          const float nref = fmaxf(ref, mx), al = ex2(ref - nref);
+          ref = nref;
+          l *= al;
 #pragma unroll 1
-            for (int c = 0; c < DH / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(t_o + 32 * c, o);
-              ld_wait();
-              pin32(o);
+          for (int c = 0; c < DH / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(t_o + 32 * c, o);
+            ld_wait();
+            pin32(o);
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float2 w = mul2(make_float2(f(o[e]), f(o[e + 1])), make_float2(al, al));
-                o[e] = __float_as_uint(w.x);
-                o[e + 1] = __float_as_uint(w.y);
-              }
-              tmem_st32(t_o + 32 * c, o);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 w = mul2(make_float2(f(o[e]), f(o[e + 1])), make_float2(al, al));
+              o[e] = __float_as_uint(w.x);
+              o[e + 1] = __float_as_uint(w.y);
             }
+            tmem_st32(t_o + 32 * c, o);
           }
         }
         const float2 c2 = make_float2(a.c, a.c), r2 = make_float2(-ref, -ref);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < KT / 32; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -434,33 +411,34 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
             sum = add2(sum, w);
             p[e] = pack_bf16(w.x, w.y);
           }
-          tmem_st16(tmem + C::p_col(buf) + lanes + 16 * c, p);
+          tmem_st16(t_s + 16 * c, p);
         }
         l += sum.x + sum.y;
-        if (key0 + KT > len) {
-          // the tile's rows behind the sequence's end hold other tokens: zero
+        if (key0 + kStep > len) {
+          // the step's rows behind the sequence's end hold other tokens: zero
           // them, so that a weight of 0 times what they hold stays 0
-          const int vs = 2 * j + 1;
+          const int vs = 2 * (h / C::kSteps) + 1;
           ok = warp_wait(&full[vs % C::kSlots], (vs / C::kSlots) & 1, a.err, &stop);
           if (!ok) break;
-          unsigned char *vt = ring + (vs % C::kSlots) * C::kSlot;
-          for (int x = 128 * (len - key0) + 16 * row; x < C::kKVBox; x += 128 * 16)
+          unsigned char *vt = ring + (vs % C::kSlots) * C::kSlot + (h % C::kSteps) * (kStep * 128);
+          for (int x = 128 * (len - key0) + 16 * row; x < kStep * 128; x += 128 * 16)
 #pragma unroll
             for (int b = 0; b < C::kBoxes; ++b) *reinterpret_cast<uint4 *>(vt + b * C::kKVBox + x) = make_uint4(0, 0, 0, 0);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         st_wait();
         tc_fence_before();
-        bar_arrive(smem_addr(&p_full[buf]));
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&p_full[i][h & 1]));
       }
       if (ok && n > 0) {
-        // (with NT == 1 o_full[0] takes a phase per tile, of which this thread
-        // may be two behind, so the last tile has a barrier of its own)
-        ok = warp_wait(&o_full[NT == 2 ? i : 1], 0, a.err, &stop);
+        // (pv_done takes a phase per step, of which this thread may be two
+        // behind, so the last step has a barrier of its own)
+        ok = warp_wait(&o_full[i], 0, a.err, &stop);
         if (ok) {
           tc_fence_after();
           const float il = 1.f / l;
-          const long orow = pos < 0 ? 0 : (long)(tok0 + pos) * a.n_q_heads + h * G + row % G;
+          const long orow = pos < 0 ? 0 : (long)(tok0 + pos) * a.n_q_heads + h_kv * G + row % G;
 #pragma unroll 1
           for (int c = 0; c < DH / 32; ++c) {
             uint32_t o[32];
