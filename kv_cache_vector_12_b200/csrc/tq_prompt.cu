@@ -35,6 +35,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "tq_tc.cuh"
 
@@ -42,6 +43,7 @@ namespace tq {
 namespace {
 
 constexpr int kStep = 64;     // keys per step: one S buffer
+constexpr int kPoly = 4;      // pairs of every 16 whose exp2 runs on the FMA pipe
 constexpr float kLazy = 8.f;  // log2 units a tile's maximum may pass the reference
 
 template <int DH>
@@ -99,8 +101,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float f(uint32_t x) { return __uint_as_float(x); }
 
-// A bounded wait; false (the error flagged, the kernel told to stop) once it
-// expires.  Only the first test is inlined: the waits are many, and the loop
+// 2^x of two numbers on the FMA pipe: x = n + f with n the nearest integer
+// (added and subtracted 1.5 2^23), a polynomial of degree 5 for 2^f on
+// [-1/2, 1/2] (minimax of the relative error, fitted by weighted least squares:
+// 2.3e-7 in fp32, what ex2.approx has), and n added to the exponent.  Below
+// 2^-126 the result is some number under 2^-125 rather than 0.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 big = make_float2(12582912.f, 12582912.f);
+  const float2 t = add2(x, big);
+  const float2 g = add2(x, mul2(add2(t, make_float2(-big.x, -big.y)), make_float2(-1.f, -1.f)));
+  float2 p = make_float2(1.3276471e-3f, 1.3276471e-3f);
+  p = fma2(p, g, make_float2(9.6755410e-3f, 9.6755410e-3f));
+  p = fma2(p, g, make_float2(5.5507131e-2f, 5.5507131e-2f));
+  p = fma2(p, g, make_float2(2.4022120e-1f, 2.4022120e-1f));
+  p = fma2(p, g, make_float2(6.9314694e-1f, 6.9314694e-1f));
+  p = fma2(p, g, make_float2(1.0000001f, 1.0000001f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// A bounded wait; false (the error flagged, the producer told to stop) once it
+// expires: every role then ends at its own next wait, at most 2 s later.  Only the first test is inlined: the waits are many, and the loop
 // and its error path would crowd the instruction cache.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned *err, int *stop) {
   if (bar_wait(bar, parity)) return true;
@@ -305,7 +328,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
         if (h >= 0 && h % C::kSteps == 0) ok = warp_wait(&full[vs], vp, a.err, &stop);
         if (ok && n < last && n % C::kSteps == 0) ok = warp_wait(&full[ks], kp, a.err, &stop);
         if (ok && h >= 0 && h < mine) ok = warp_wait(&p_full[i][h & 1], (h >> 1) & 1, a.err, &stop);
-        if (!ok || __shfl_sync(0xffffffffu, *(volatile int *)&stop, 0)) break;
+        if (!ok) break;
         tc_fence_after();
         const bool v_end = h >= 0 && h % C::kSteps == C::kSteps - 1, k_end = n < last && n % C::kSteps == C::kSteps - 1;
         if (elect_one()) {
@@ -314,7 +337,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kStep / 16; ++kk)  // 16 tokens: 2048 bytes
               mma_ts(d_o, d_s + 64u * (h & 1) + 8 * kk, v + kk * (2048 >> 4), C::idesc_o, (h > 0 || kk > 0) ? 1u : 0u);
-            tc_commit(smem_addr(&pv_done[i]));
+            if (h + 2 == mine) tc_commit(smem_addr(&pv_done[i]));
             if (h + 1 == mine) tc_commit(smem_addr(&o_full[i]));
           }
           if (v_end) tc_commit(smem_addr(&empty[vs]));
@@ -349,10 +372,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
       for (int h = 0; h < n; ++h) {
         const uint32_t t_s = C::s_col(i, h & 1) + lanes;
         ok = warp_wait(&s_full[i][h & 1], (h >> 1) & 1, a.err, &stop);
-        if (!ok || *(volatile int *)&stop) {
-          ok = false;
-          break;
-        }
+        if (!ok) break;
         tc_fence_after();
         uint32_t v[2][32];
 #pragma unroll
@@ -377,8 +397,11 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
         if (h == 0) {
           ref = fmaxf(mx, -3.0e38f);
         } else if (__any_sync(0xffffffffu, mx > ref + kLazy)) {
-          // O is rescaled once the values of step h - 1 are in it
-          ok = warp_wait(&pv_done[i], (h - 1) & 1, a.err, &stop);
+          // O is rescaled once the values of step h - 1 are in it: the scores of
+          // step h + 1 were issued behind them (in front of the last step nothing
+          // was, so those have a barrier of their own)
+          ok = h + 1 < n ? warp_wait(&s_full[i][(h + 1) & 1], ((h + 1) >> 1) & 1, a.err, &stop)
+                         : warp_wait(&pv_done[i], 0, a.err, &stop);
           if (!ok) break;
           tc_fence_after();
           const float nref = fmaxf(ref, mx), al = ex2(ref - nref);
@@ -401,18 +424,27 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
         }
         const float2 c2 = make_float2(a.c, a.c), r2 = make_float2(-ref, -ref);
         float2 sum = make_float2(0.f, 0.f);
+        // kPoly of every 16 pairs on the FMA pipe, the others on the MUFU (16 a
+        // clock and SM: 64 scores of a warp take it 512 cycles); steps with
+        // masked scores, whose weights have to be exactly 0, all on the MUFU
+        auto weights = [&](auto mixed) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[16];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = fma2(make_float2(f(v[c][2 * e]), f(v[c][2 * e + 1])), c2, r2);
-            const float2 w = make_float2(ex2(x.x), ex2(x.y));
-            sum = add2(sum, w);
-            p[e] = pack_bf16(w.x, w.y);
+            for (int e = 0; e < 16; ++e) {
+              const float2 x = fma2(make_float2(f(v[c][2 * e]), f(v[c][2 * e + 1])), c2, r2);
+              float2 w;
+              if (decltype(mixed)::value && e % (16 / kPoly) == 1) w = exp2_fma(x);
+              else w = make_float2(ex2(x.x), ex2(x.y));
+              sum = add2(sum, w);
+              p[e] = pack_bf16(w.x, w.y);
+            }
+            tmem_st16(t_s + 16 * c, p);
           }
-          tmem_st16(t_s + 16 * c, p);
-        }
+        };
+        if (key0 + kStep - 1 > base) weights(std::false_type{});
+        else weights(std::true_type{});
         l += sum.x + sum.y;
         if (key0 + kStep > len) {
           // the step's rows behind the sequence's end hold other tokens: zero
@@ -432,8 +464,6 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
         if (lane == 0) bar_arrive(smem_addr(&p_full[i][h & 1]));
       }
       if (ok && n > 0) {
-        // (pv_done takes a phase per step, of which this thread may be two
-        // behind, so the last step has a barrier of its own)
         ok = warp_wait(&o_full[i], 0, a.err, &stop);
         if (ok) {
           tc_fence_after();
