@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kTabThreads = 512;
 constexpr int kTabWarps = kTabThreads / 32;
-constexpr int kTokVec = 4;  // consecutive tokens of one thread: 16-byte stores
 
 struct TablesArgs {
   unsigned *err;
@@ -40,8 +39,19 @@ struct TablesArgs {
   int32_t *seq_idx, *pos;
   int64_t *slots;           // or null
   int32_t *cu_new, *seq_lens;
-  bool vec;                 // every per-token output is 16-byte aligned
+  uint32_t div_mul;         // x / block_size = umulhi(x, div_mul) >> div_shift
+  int div_shift;
 };
+
+// Division by the block size without the divide's code: a launch starts with
+// cold instruction caches, and a run of a few microseconds pays for every line.
+__device__ __forceinline__ int block_of(const TablesArgs &a, int x) {
+  return (int)(a.div_mul ? __umulhi((unsigned)x, a.div_mul) >> a.div_shift : (unsigned)x >> a.div_shift);
+}
+// Blocks that x tokens fill or begin.
+__device__ __forceinline__ int blocks_of(const TablesArgs &a, int x) {
+  return x > 0 ? block_of(a, x - 1) + 1 : 0;
+}
 
 // Sums of lengths that may pass 2^31 saturate there: any such total is past
 // the outputs' end anyway.  (Both terms are in [0, INT_MAX].)
@@ -67,8 +77,6 @@ __device__ __forceinline__ int last_at_most(const int *cu, int n, int x) {
   return lo;
 }
 
-__device__ __forceinline__ int blocks_of(int tokens, int bs) { return tokens / bs + (tokens % bs != 0); }
-
 // The lengths of sequence s as the call uses them: a sequence whose lengths
 // are negative or pass the capacity gets no tokens and length 0.
 __device__ __forceinline__ bool lengths_of(const TablesArgs &a, int s, int &c, int &w) {
@@ -89,6 +97,7 @@ __device__ __forceinline__ int take_block(const TablesArgs &a, int start, int i)
   return -1;
 }
 
+template <bool VEC>
 __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesArgs a) {
   // [n_seqs + 1] W, [n_seqs + 1] T, [n_seqs] c, [n_groups + 1] group bounds
   extern __shared__ int s_dyn[];
@@ -103,6 +112,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
     bad |= !lengths_of(a, s, c, w);
     s_c[s] = c;
     s_tok[s] = w;
+    s_blk[s] = paged ? blocks_of(a, c + w) - blocks_of(a, c) : 0;
     if (blockIdx.x == 0) a.seq_lens[s] = c + w;
   }
   for (int g = tid; g <= a.n_groups; g += kTabThreads)
@@ -112,119 +122,75 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
     start = *a.free_start;
     if (start < 0 || start > a.n_free) start = a.n_free;
   }
-  __syncthreads();
-
-  // ---- the two exclusive sums; thread t takes a run of consecutive sequences
-  const int run = (a.n_seqs + kTabThreads - 1) / kTabThreads;
-  const int s0 = min(tid * run, a.n_seqs), s1 = min(s0 + run, a.n_seqs);
-  int tok = 0, blk = 0;
-  for (int s = s0; s < s1; ++s) {
-    const int c = s_c[s], w = s_tok[s];
-    s_blk[s] = paged ? blocks_of(c + w, a.block_size) - blocks_of(c, a.block_size) : 0;
-    tok = sat_add(tok, w);
-    blk = sat_add(blk, s_blk[s]);
-  }
   if (bad && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
-  const int itok = warp_inclusive(tok, lane), iblk = warp_inclusive(blk, lane);
-  if (lane == 31) {
-    s_sum[0][warp] = itok;
-    s_sum[1][warp] = iblk;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const int v0 = lane < kTabWarps ? s_sum[0][lane] : 0, v1 = lane < kTabWarps ? s_sum[1][lane] : 0;
-    const int i0 = warp_inclusive(v0, lane), i1 = warp_inclusive(v1, lane);
-    if (lane < kTabWarps) {
-      s_sum[0][lane] = i0;
-      s_sum[1][lane] = i1;
-    }
-  }
-  __syncthreads();
-  int btok = warp ? s_sum[0][warp - 1] : 0, bblk = warp ? s_sum[1][warp - 1] : 0;
-  {
-    const int utok = __shfl_up_sync(0xffffffffu, itok, 1), ublk = __shfl_up_sync(0xffffffffu, iblk, 1);
-    if (lane) {
-      btok = sat_add(btok, utok);
-      bblk = sat_add(bblk, ublk);
-    }
-  }
-  for (int s = s0; s < s1; ++s) {
-    const int w = s_tok[s], t = s_blk[s];
-    s_tok[s] = btok;
-    s_blk[s] = bblk;
-    if (blockIdx.x == 0) a.cu_new[s] = btok;
-    btok = sat_add(btok, w);
-    bblk = sat_add(bblk, t);
-  }
-  const int total_tok = s_sum[0][kTabWarps - 1], total_blk = s_sum[1][kTabWarps - 1];
-  if (tid == 0) {
-    s_tok[a.n_seqs] = total_tok;
-    s_blk[a.n_seqs] = total_blk;
-    if (blockIdx.x == 0) {
-      a.cu_new[a.n_seqs] = total_tok;
-      if (paged) *a.free_end = (int)min((long)start + total_blk, (long)a.n_free);
-      if (total_tok > a.n_tok) atomicOr(a.err, kErrTokenRange);
-    }
-  }
   __syncthreads();
 
-  // ---- per-token maps: kTokVec consecutive rows per thread
+  // ---- the two exclusive sums, side by side: half of the threads takes the
+  // tokens, half the blocks, every thread a run of consecutive sequences
+  {
+    constexpr int kHalf = kTabThreads / 2, kHalfWarps = kTabWarps / 2;
+    const int half = tid / kHalf, t = tid % kHalf, hw = t >> 5;
+    int *v = half ? s_blk : s_tok;
+    const int run = (a.n_seqs + kHalf - 1) / kHalf;
+    const int s0 = min(t * run, a.n_seqs), s1 = min(s0 + run, a.n_seqs);
+    int sum = 0;
+    for (int s = s0; s < s1; ++s) sum = sat_add(sum, v[s]);
+    const int inc = warp_inclusive(sum, lane);
+    if (lane == 31) s_sum[half][hw] = inc;
+    int excl = __shfl_up_sync(0xffffffffu, inc, 1);
+    if (lane == 0) excl = 0;
+    __syncthreads();
+    for (int w = 0; w < hw; ++w) excl = sat_add(excl, s_sum[half][w]);
+    for (int s = s0; s < s1; ++s) {
+      const int x = v[s];
+      v[s] = excl;
+      if (half == 0 && blockIdx.x == 0) a.cu_new[s] = excl;
+      excl = sat_add(excl, x);
+    }
+    if (t == kHalf - 1) v[a.n_seqs] = excl;  // (runs past the end are empty: the total)
+  }
+  __syncthreads();
+  const int total_tok = s_tok[a.n_seqs], total_blk = s_blk[a.n_seqs];
+  if (tid == 0 && blockIdx.x == 0) {
+    a.cu_new[a.n_seqs] = total_tok;
+    if (paged) *a.free_end = (int)min((long)start + total_blk, (long)a.n_free);
+    if (total_tok > a.n_tok) atomicOr(a.err, kErrTokenRange);
+  }
+
+  // ---- per-token maps: a row per thread, or (VEC) four, in one 16-byte store
+  // per map (two for the slots) where they lie in one block of one sequence
+  constexpr int kTokVec = VEC ? 4 : 1;
   const int rows = min(total_tok, a.n_tok);
   const int stride = gridDim.x * kTabThreads;
-  const int n_vec = (rows + kTokVec - 1) / kTokVec;
-  for (int v = blockIdx.x * kTabThreads + tid; v < n_vec; v += stride) {
-    const int r0 = v * kTokVec;
+  auto slot_of = [&](int s, int c, int p) -> long {
+    if (!paged) return (long)s * a.capacity + p;
+    const int j = block_of(a, p), first = blocks_of(a, c);
+    // a block of this call, or the one that the cached tokens end in
+    const int b = j >= first ? take_block(a, start, s_blk[s] + (j - first)) : a.table[(long)s * a.per_seq + j];
+    if (b >= 0 && b < a.n_blocks) return (long)b * a.block_size + (p - j * a.block_size);
+    atomicOr(a.err, kErrTokenRange);
+    return -1;
+  };
+#pragma unroll 1
+  for (int r0 = kTokVec * (blockIdx.x * kTabThreads + tid); r0 < rows; r0 += kTokVec * stride) {
     int s = last_at_most(s_tok, a.n_seqs, r0);
-    int c = s_c[s], j = -1, b = -1;  // j: the logical block that b is for
-    int sq[kTokVec], ps[kTokVec];
-    long sl[kTokVec];
-#pragma unroll
-    for (int e = 0; e < kTokVec; ++e) {
-      const int r = min(r0 + e, rows - 1);
-      while (r >= s_tok[s + 1]) {  // the next sequence with tokens
-        c = s_c[++s];
-        j = -1;
-      }
-      const int p = c + (r - s_tok[s]);
-      sq[e] = s;
-      ps[e] = p;
-      if (!paged) {
-        sl[e] = (long)s * a.capacity + p;
-      } else if (a.slots) {
-        const int jp = p / a.block_size;
-        if (jp != j) {
-          j = jp;
-          const int first = blocks_of(c, a.block_size);
-          if (j >= first) {
-            b = take_block(a, start, s_blk[s] + (j - first));
-          } else {  // the block that the cached tokens end in
-            b = a.table[(long)s * a.per_seq + j];
-            if (b < 0 || b >= a.n_blocks) {
-              atomicOr(a.err, kErrTokenRange);
-              b = -1;
-            }
-          }
-        }
-        sl[e] = b < 0 ? -1 : (long)b * a.block_size + (p - j * a.block_size);
-      } else {
-        sl[e] = -1;
-      }
-    }
-    if (a.vec && r0 + kTokVec <= rows) {
-      *reinterpret_cast<int4 *>(a.seq_idx + r0) = make_int4(sq[0], sq[1], sq[2], sq[3]);
-      *reinterpret_cast<int4 *>(a.pos + r0) = make_int4(ps[0], ps[1], ps[2], ps[3]);
+    const int c = s_c[s], p = c + (r0 - s_tok[s]);
+    if (VEC && r0 + kTokVec <= min(rows, s_tok[s + 1]) && block_of(a, p) == block_of(a, p + kTokVec - 1)) {
+      *reinterpret_cast<int4 *>(a.seq_idx + r0) = make_int4(s, s, s, s);
+      *reinterpret_cast<int4 *>(a.pos + r0) = make_int4(p, p + 1, p + 2, p + 3);
       if (a.slots) {
-        *reinterpret_cast<longlong2 *>(a.slots + r0) = make_longlong2(sl[0], sl[1]);
-        *reinterpret_cast<longlong2 *>(a.slots + r0 + 2) = make_longlong2(sl[2], sl[3]);
+        const long x = slot_of(s, c, p), d = x < 0 ? 0 : 1;
+        *reinterpret_cast<longlong2 *>(a.slots + r0) = make_longlong2(x, x + d);
+        *reinterpret_cast<longlong2 *>(a.slots + r0 + 2) = make_longlong2(x + 2 * d, x + 3 * d);
       }
     } else {
-#pragma unroll
-      for (int e = 0; e < kTokVec; ++e) {
-        if (r0 + e < rows) {
-          a.seq_idx[r0 + e] = sq[e];
-          a.pos[r0 + e] = ps[e];
-          if (a.slots) a.slots[r0 + e] = sl[e];
-        }
+#pragma unroll 1
+      for (int r = r0; r < min(r0 + kTokVec, rows); ++r) {
+        while (r >= s_tok[s + 1]) ++s;  // the next sequence with tokens
+        const int q = s_c[s] + (r - s_tok[s]);
+        a.seq_idx[r] = s;
+        a.pos[r] = q;
+        if (a.slots) a.slots[r] = slot_of(s, s_c[s], q);
       }
     }
   }
@@ -233,7 +199,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
   // ---- new table entries, one per thread
   for (int i = blockIdx.x * kTabThreads + tid; i < total_blk; i += stride) {
     const int s = last_at_most(s_blk, a.n_seqs, i);
-    a.table[(long)s * a.per_seq + blocks_of(s_c[s], a.block_size) + (i - s_blk[s])] = take_block(a, start, i);
+    a.table[(long)s * a.per_seq + blocks_of(a, s_c[s]) + (i - s_blk[s])] = take_block(a, start, i);
   }
 
   // ---- shared prefixes: every member but the first takes the first one's
@@ -249,12 +215,12 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
     // (lengths out of bounds count as 0 here, and were flagged above)
     const int cl = lead >= 0 ? s_c[lead] : 0;
     const int tl = lead >= 0 ? cl + (s_tok[lead + 1] - s_tok[lead]) : 0;
-    if (prefix < 0 || prefix % a.block_size != 0 || prefix > s_c[s] || prefix > tl) {
+    if (prefix < 0 || block_of(a, prefix) * a.block_size != prefix || prefix > s_c[s] || prefix > tl) {
       if (lane == 0) atomicOr(a.err, kErrSeqLen);
       continue;
     }
-    const int held = blocks_of(cl, a.block_size);
-    const int n = prefix / a.block_size;
+    const int held = blocks_of(a, cl);
+    const int n = block_of(a, prefix);
     const int32_t *src = a.table + (long)lead * a.per_seq;
     int32_t *dst = a.table + (long)s * a.per_seq;
     constexpr int kBatch = 8;  // loads of a lane in flight ahead of its stores
@@ -275,11 +241,11 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
 
 }  // namespace
 
-// One CTA per 2048 tokens (a thread's four), and with groups one per 16
-// sequences (a warp's one), at most four per SM (what its threads allow): a
-// decode step of a few sequences is a single CTA, a million prompt tokens are
-// in flight at once.  Measured for 1.05 M tokens of 32 prompts: one CTA per SM
-// 9.9 us, four 6.0.
+// A thread per token, and with groups a warp per sequence, up to the CTAs that
+// are resident at once (four per SM): a decode step of up to 512 tokens without
+// groups is a single CTA.  More tokens than resident threads (prompts, whose rows
+// run on in one block) are taken four to a thread: 1.05 M tokens 8.6 us, and 9.7
+// with one to a thread; a step of 32 sequences 3.6 us with four, 2.4 with one.
 int launch_tables(const DeviceParams &p, const tq_cache &c, int32_t *block_table, const int32_t *cached,
                   const int32_t *fresh, const int32_t *free_list, int n_free, const int32_t *free_start,
                   int32_t *free_end, const int32_t *cu_group, const int32_t *prefix, int n_groups, int n_tok,
@@ -307,13 +273,28 @@ int launch_tables(const DeviceParams &p, const tq_cache &c, int32_t *block_table
   a.slots = slots;
   a.cu_new = cu_new;
   a.seq_lens = seq_lens;
-  a.vec = (((uintptr_t)seq_idx | (uintptr_t)pos | (uintptr_t)slots) & 15u) == 0;
-  long ctas = ((long)n_tok + kTabThreads * kTokVec - 1) / (kTabThreads * kTokVec);
+  // floor(x / d) for 0 <= x < 2^31: a shift for powers of two, else with s the
+  // bits of d - 1 and m = ceil(2^(31 + s) / d) < 2^32 it is m x >> (31 + s), as
+  // m d - 2^(31 + s) < d <= 2^s
+  const unsigned d = (unsigned)a.block_size;
+  int bits = 0;
+  while ((1u << bits) < d) ++bits;
+  if ((1u << bits) == d) {
+    a.div_mul = 0;
+    a.div_shift = bits;
+  } else {
+    a.div_mul = (uint32_t)(((1ull << (31 + bits)) + d - 1) / d);
+    a.div_shift = bits - 1;
+  }
+  const long sms = sm_count();
+  const bool vec =
+      n_tok > 4 * sms * kTabThreads && (((uintptr_t)seq_idx | (uintptr_t)pos | (uintptr_t)slots) & 15u) == 0;
+  const long per_cta = (vec ? 4 : 1) * kTabThreads;
+  long ctas = ((long)n_tok + per_cta - 1) / per_cta;
   if (a.n_groups > 0) {
     const long by_seq = ((long)c.n_seqs + kTabWarps - 1) / kTabWarps;
     ctas = ctas > by_seq ? ctas : by_seq;
   }
-  const long sms = sm_count();
   ctas = ctas < 1 ? 1 : ctas > 4 * sms ? 4 * sms : ctas;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -322,10 +303,11 @@ int launch_tables(const DeviceParams &p, const tq_cache &c, int32_t *block_table
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kTabThreads);
   const size_t words = 3 * (size_t)c.n_seqs + 2 + (size_t)a.n_groups + 1;
-  static std::atomic<bool> configured[kMaxDevices];
-  std::atomic<bool> &done = configured[current_device()];
+  const auto kernel = vec ? build_tables_kernel<true> : build_tables_kernel<false>;
+  static std::atomic<bool> configured[kMaxDevices][2];
+  std::atomic<bool> &done = configured[current_device()][vec];
   if (!done.load(std::memory_order_acquire)) {  // more than 48 KB from about 3000 sequences in groups on
-    const cudaError_t e = cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)((4 * (size_t)kMaxTableSeqs + 3) * sizeof(int)));
     if (e != cudaSuccess) return (int)e;
     done.store(true, std::memory_order_release);
@@ -334,7 +316,7 @@ int launch_tables(const DeviceParams &p, const tq_cache &c, int32_t *block_table
   cfg.stream = (cudaStream_t)stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, build_tables_kernel, a);
+  return (int)cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace tq

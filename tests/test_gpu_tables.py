@@ -118,6 +118,15 @@ def test_unaligned_outputs_rows_behind_the_last_and_no_slots(tq, ctx, offset):
     run_paged(tq, ctx, [5, 0, 100], [60, 7, 33], 64, 192, extra_rows=3, offset=offset, with_slots=False)
 
 
+def test_more_tokens_than_resident_threads(tq, ctx):
+    """Four rows to a thread: sequences that begin and end inside its four, blocks that do, unaligned outputs."""
+    rng = np.random.default_rng(0)
+    for offset in (0, 1):
+        cached, new = rng.integers(0, 500, 90).tolist(), rng.integers(0, 9000, 90).tolist()
+        new[3:9] = [1, 0, 2, 3, 0, 1]
+        run_paged(tq, ctx, cached, new, 64, 9600, seed=offset, offset=offset)
+
+
 def test_shared_prefixes(tq, ctx):
     """Groups of one to many members; a first member that gets its prefix in
     this call; a prefix of zero; sequences behind the last group."""
