@@ -42,26 +42,38 @@
 namespace tq {
 namespace {
 
+// longest prompt up to which the form with one row tile runs.  Measured, 32768
+// tokens of prompts of 1 .. n tokens, 8 KV and 32 query heads, one row tile / two:
+// d = 64, n = 256 107 / 136 us, 1024 157 / 172, 2048 229 / 229, 4096 452 / 428;
+// d = 128, n = 256 138 / 174, 512 170 / 190, 1024 212 / 210, 4096 640 / 452.
+constexpr int kSmallLen64 = 2048, kSmallLen128 = 768;
 constexpr int kStep = 64;     // keys per step: one S buffer
 constexpr int kPoly = 4;      // pairs of every 16 whose exp2 runs on the FMA pipe
 constexpr float kLazy = 8.f;  // log2 units a tile's maximum may pass the reference
 
-template <int DH>
+// Two forms.  With two row tiles (d = 64 and 128) a CTA fills an SM and shares
+// K and V between them: long prompts.  With one row tile, tiles of 64 keys and
+// half of tensor memory two CTAs fit an SM (d = 64 and 128), so that the start
+// and the end of one run under the other: short prompts.  At d = 256 O takes
+// half of tensor memory for one row tile, and a CTA the SM.
+template <int DH, int ROWS>
 struct PromptCfg {
-  static constexpr int NT = DH == 256 ? 1 : 2;      // row tiles of 128
-  static constexpr int KT = DH == 256 ? 64 : 128;   // keys per tile of K or V
+  static constexpr int NT = ROWS;                   // row tiles of 128
+  static constexpr int KT = NT == 1 ? 64 : 128;     // keys per tile of K or V
   static constexpr int kSteps = KT / kStep;         // steps per tile
+  static constexpr int kPerSm = NT == 1 && DH < 256 ? 2 : 1;  // CTAs per SM
   static constexpr int kBoxes = DH / 64;            // 64-column swizzled boxes per operand
   static constexpr int kQBox = 128 * 128;           // bytes of one box of a Q tile
   static constexpr int kKVBox = KT * 128;           // bytes of one box of a K or V tile
   static constexpr int kQTile = kBoxes * kQBox;
   static constexpr int kSlot = kBoxes * kKVBox;
-  static constexpr int kSlots = DH == 64 ? 8 : 5;
+  static constexpr int kSlots = DH == 64 ? (NT == 2 ? 8 : 5) : DH == 128 && NT == 1 ? 4 : 5;  // at least 4
   static constexpr int kSoftWarps = 4 * NT;
   static constexpr int kProdWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
   static constexpr int kThreads = 32 * (kSoftWarps + 1 + NT);  // an MMA warp per row tile
   static constexpr int smem = 1024 + NT * kQTile + kSlots * kSlot;
   // tensor-memory columns: two S buffers per row tile (P over them) and O
+  static constexpr uint32_t kCols = NT * (128u + DH) <= 256 ? 256 : 512;
   static constexpr uint32_t s_col(int i, int b) { return 128u * i + 64u * b; }
   static constexpr uint32_t o_col(int i) { return 128u * NT + (uint32_t)DH * i; }
   // instruction descriptors, kind::f16: bf16 A and B, fp32 D, M = 128; S has
@@ -175,12 +187,16 @@ __device__ __forceinline__ void find_block(const PromptArgs &a, int span, int x,
       blk = lo;
     }
   } else {
-    int done = 0;  // blocks of the sequences before s0
-    for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-      const int i = s0 + lane;
-      bad = false;
-      const int nb = i < a.n_seqs ? blocks_of_seq(a, i, span, bad) : 0;
-      any_bad |= bad;
+    // each lane counts the blocks of a run of sequences, the run that holds
+    // block x is cut into 32 again, until a run is one sequence
+    int lo = 0, count = a.n_seqs, done = 0;  // done: blocks of the sequences before lo
+    for (bool first = true;; first = false) {
+      const int run = (count + 31) / 32, b = min(lane * run, count), e = min(b + run, count);
+      int nb = 0;
+      for (int i = b; i < e; ++i) {
+        nb += blocks_of_seq(a, lo + i, span, bad);
+        if (first) any_bad |= bad;
+      }
       int inc = nb;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -188,23 +204,26 @@ __device__ __forceinline__ void find_block(const PromptArgs &a, int span, int x,
         if (lane >= o) inc += u;
       }
       const unsigned past = __ballot_sync(0xffffffffu, done + inc > x);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        s = s0 + l;
-        blk = done + __shfl_sync(0xffffffffu, inc, l) - 1 - x;  // from the sequence's end
+      if (!past) break;
+      const int l = __ffs(past) - 1, end = done + __shfl_sync(0xffffffffu, inc, l);
+      if (run == 1) {
+        s = lo + l;
+        blk = end - 1 - x;  // from the sequence's end
         break;
       }
-      done += __shfl_sync(0xffffffffu, inc, 31);
+      done = end - __shfl_sync(0xffffffffu, nb, l);
+      lo += l * run;
+      count = min(run, count - l * run);
     }
   }
   if (any_bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrSeqLen);
 }
 
-template <int DH>
-__global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
+template <int DH, int ROWS>
+__global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, ROWS>::kPerSm)
     prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
-  using C = PromptCfg<DH>;
+  using C = PromptCfg<DH, ROWS>;
   constexpr int NT = C::NT, KT = C::KT;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -227,7 +246,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
     }
   } else if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
-                 "r"(512u)
+                 "r"(C::kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == C::kProdWarp && lane == 0) {
@@ -250,7 +269,8 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // (all 512 columns are this CTA's: addresses start at column 0 of lane 0)
+  // (with all 512 columns this CTA's, they start at column 0)
+  const uint32_t tmem = C::kCols == 512 ? 0u : tmem_slot;
   const int s = s_seq;
 
   if (s >= 0) {
@@ -315,7 +335,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
       };
       const uint64_t q = sw128_desc(smem_addr(sm + i * C::kQTile));
       const uint64_t k0 = sw128_desc(smem_addr(ring)), v0 = mn_desc(smem_addr(ring), C::kKVBox);
-      const uint32_t d_o = C::o_col(0) + (uint32_t)DH * i, d_s = 128u * i;
+      const uint32_t d_o = tmem + C::o_col(0) + (uint32_t)DH * i, d_s = tmem + 128u * i;
       constexpr int kSlotU = C::kSlot >> 4, kStepU = (kStep * 128) >> 4;  // descriptor units
       // Step h: O += P V, then S of step h + 2 over the P just read (MMAs of one
       // thread run in order); two S go ahead.  A tile's slot is given back after
@@ -365,12 +385,12 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
       const int n = steps[i], base = first + i * PC;
       const int t = row / G, pos = (row < PC * G && base + t < len) ? base + t : -1;
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-      const uint32_t t_o = C::o_col(i) + lanes;
+      const uint32_t t_o = tmem + C::o_col(i) + lanes;
       float ref = 0.f, l = 0.f;
       bool ok = true;
 #pragma unroll 1
       for (int h = 0; h < n; ++h) {
-        const uint32_t t_s = C::s_col(i, h & 1) + lanes;
+        const uint32_t t_s = tmem + C::s_col(i, h & 1) + lanes;
         ok = warp_wait(&s_full[i][h & 1], (h >> 1) & 1, a.err, &stop);
         if (!ok) break;
         tc_fence_after();
@@ -502,7 +522,7 @@ __global__ void __launch_bounds__(PromptCfg<DH>::kThreads, 1)
   __syncthreads();
   if (warp == C::kMmaWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(512u) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(C::kCols) : "memory");
   }
 }
 
@@ -521,10 +541,10 @@ bool make_token_map(CUtensorMap *m, const void *base, int d, int heads, long tok
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DH>
-int launch(const PromptArgs &args, const void *q, const void *k, const void *v, long qs, long ks, long vs,
+template <int DH, int ROWS>
+int launch(PromptArgs args, const void *q, const void *k, const void *v, long qs, long ks, long vs,
            void *stream) {
-  using C = PromptCfg<DH>;
+  using C = PromptCfg<DH, ROWS>;
   const int G = args.n_q_heads / args.n_kv_heads;
   CUtensorMap mq, mk, mv;
   if (!make_token_map(&mq, q, DH, args.n_q_heads, args.n_tok, qs, G, args.per_tile) ||
@@ -534,7 +554,7 @@ int launch(const PromptArgs &args, const void *q, const void *k, const void *v, 
   static std::atomic<bool> configured[kMaxDevices];
   std::atomic<bool> &done = configured[current_device()];
   if (!done.load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+    const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<DH, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
     if (e != cudaSuccess) return (int)e;
     done.store(true, std::memory_order_release);
   }
@@ -551,7 +571,7 @@ int launch(const PromptArgs &args, const void *q, const void *k, const void *v, 
   cfg.stream = (cudaStream_t)stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, prompt_kernel<DH>, args, mq, mk, mv);
+  return (int)cudaLaunchKernelEx(&cfg, prompt_kernel<DH, ROWS>, args, mq, mk, mv);
 }
 
 }  // namespace
@@ -572,9 +592,13 @@ int launch_prompt(const DeviceParams &p, const void *q, const void *k, const voi
   a.out = out;
   a.out_f32 = out_f32;
   a.lse = lse;
-  if (p.d == 64) return launch<64>(a, q, k, v, q_stride, k_stride, v_stride, stream);
-  if (p.d == 256) return launch<256>(a, q, k, v, q_stride, k_stride, v_stride, stream);
-  return launch<128>(a, q, k, v, q_stride, k_stride, v_stride, stream);
+  const bool small = max_len <= (p.d == 64 ? kSmallLen64 : kSmallLen128);
+  if (p.d == 256) return launch<256, 1>(a, q, k, v, q_stride, k_stride, v_stride, stream);
+  if (p.d == 64)
+    return small ? launch<64, 1>(a, q, k, v, q_stride, k_stride, v_stride, stream)
+                 : launch<64, 2>(a, q, k, v, q_stride, k_stride, v_stride, stream);
+  return small ? launch<128, 1>(a, q, k, v, q_stride, k_stride, v_stride, stream)
+               : launch<128, 2>(a, q, k, v, q_stride, k_stride, v_stride, stream);
 }
 
 }  // namespace tq

@@ -159,6 +159,18 @@ def test_many_prompts(tq, n):
     run(tq, rng.integers(0, 150, n).tolist(), 2, 4, 128, seed=n)
 
 
+@pytest.mark.parametrize("n", [1023, 1100, 2500])
+def test_more_prompts_than_a_warp_squared(tq, n):
+    rng = np.random.default_rng(n)
+    run(tq, (rng.integers(0, 9, n) * rng.integers(0, 2, n)).tolist() + [70], 1, 2, 64, seed=n)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [767, 768, 769, 2047, 2048, 2049])
+def test_either_side_of_the_form_for_short_prompts(tq, d, n):
+    run(tq, [n, 300, 0, 65], 1, 4, d, seed=n)
+
+
 def test_a_nan_in_a_prompt_stays_in_it_and_after_its_tile(tq):
     ctx = context(tq, 128)
     lens = [400, 300]
