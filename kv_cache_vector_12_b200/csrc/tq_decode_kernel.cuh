@@ -312,6 +312,8 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
     const bool last = a.beside && (int)blockIdx.z == a.c.n_seqs;
     if (last ? blockIdx.x + blockIdx.y == 0 : !a.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (last) return;
+    // (no line of theirs that this SM may still hold from an earlier kernel is read)
+    if (a.beside) __threadfence();
     if (a.pass == kPassPrefix) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");

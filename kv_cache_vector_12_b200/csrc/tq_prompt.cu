@@ -160,12 +160,40 @@ __device__ __forceinline__ int blocks_of_seq(const PromptArgs &a, int s, int spa
   return bad ? 0 : (e - b + span - 1) / span;
 }
 
+__device__ __forceinline__ int inclusive(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// Blocks of the run of sequences that thread t counts for find_block.
+template <int kThreads>
+__device__ __forceinline__ int count_run(const PromptArgs &a, int span, int t) {
+  const int run = (a.n_seqs + kThreads - 1) / kThreads, b = min(t * run, a.n_seqs), e = min(b + run, a.n_seqs);
+  int n = 0;
+  bool bad, any_bad = false;
+#pragma unroll 4
+  for (int i = b; i < e; ++i) {
+    n += blocks_of_seq(a, i, span, bad);
+    any_bad |= bad;
+  }
+  if (any_bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrSeqLen);
+  return n;
+}
+
 // The sequence and query block of CTA x, by one warp; s = -1 when there is
 // none.  Blocks with more keys come first, so that the last CTAs to start are
 // the shortest: within a sequence from its end, and with at most 32 sequences
 // (one per lane) across them too.  F(L) = sum_s max(0, blocks_s - L) blocks lie
 // at level L or above; the CTA's level is the largest L with F(L) > x.
-__device__ __forceinline__ void find_block(const PromptArgs &a, int span, int x, int lane, int &s, int &blk) {
+// With more than 32, part[t] holds the blocks of run t of kThreads equal runs of
+// sequences, counted by thread t beforehand.
+template <int kThreads>
+__device__ __forceinline__ void find_block(const PromptArgs &a, int span, int x, int lane, const int *part, int &s,
+                                           int &blk) {
   s = -1;
   blk = 0;
   bool bad = false, any_bad = false;
@@ -187,33 +215,26 @@ __device__ __forceinline__ void find_block(const PromptArgs &a, int span, int x,
       blk = lo;
     }
   } else {
-    // each lane counts the blocks of a run of sequences, the run that holds
-    // block x is cut into 32 again, until a run is one sequence
-    int lo = 0, count = a.n_seqs, done = 0;  // done: blocks of the sequences before lo
-    for (bool first = true;; first = false) {
-      const int run = (count + 31) / 32, b = min(lane * run, count), e = min(b + run, count);
-      int nb = 0;
-      for (int i = b; i < e; ++i) {
-        nb += blocks_of_seq(a, lo + i, span, bad);
-        if (first) any_bad |= bad;
-      }
-      int inc = nb;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
-      }
+    // the run that holds block x, then the sequence in it
+    const int run = (a.n_seqs + kThreads - 1) / kThreads;
+    int done = 0, lo = -1;  // done: blocks of the sequences before lo
+    for (int t0 = 0; t0 < kThreads && lo < 0; t0 += 32) {
+      const int n = part[t0 + lane], inc = inclusive(n, lane);
       const unsigned past = __ballot_sync(0xffffffffu, done + inc > x);
-      if (!past) break;
-      const int l = __ffs(past) - 1, end = done + __shfl_sync(0xffffffffu, inc, l);
-      if (run == 1) {
-        s = lo + l;
+      const int l = past ? __ffs(past) - 1 : 31;
+      done += __shfl_sync(0xffffffffu, past ? inc - n : inc, l);
+      if (past) lo = (t0 + l) * run;
+    }
+    for (int i0 = 0; lo >= 0 && s < 0 && i0 < run; i0 += 32) {
+      const int i = lo + i0 + lane;
+      const int n = i0 + lane < run && i < a.n_seqs ? blocks_of_seq(a, i, span, bad) : 0, inc = inclusive(n, lane);
+      const unsigned past = __ballot_sync(0xffffffffu, done + inc > x);
+      const int l = past ? __ffs(past) - 1 : 31, end = done + __shfl_sync(0xffffffffu, inc, l);
+      if (past) {
+        s = lo + i0 + l;
         blk = end - 1 - x;  // from the sequence's end
-        break;
       }
-      done = end - __shfl_sync(0xffffffffu, nb, l);
-      lo += l * run;
-      count = min(run, count - l * run);
+      done = end;
     }
   }
   if (any_bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrSeqLen);
@@ -231,14 +252,23 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
   __shared__ __align__(8) uint64_t q_full, full[C::kSlots], empty[C::kSlots];
   __shared__ __align__(8) uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], fin[2];  // [row tile][buffer]
   __shared__ uint32_t tmem_slot;
-  __shared__ int stop, s_seq, s_blk;
+  __shared__ int stop, s_seq, s_blk, s_part[C::kThreads];
 
   const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31, h_kv = blockIdx.y;
   const int G = a.n_q_heads / a.n_kv_heads, PC = a.per_tile, span = NT * PC;
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.n_seqs > 32) {
+    s_part[tid] = count_run<C::kThreads>(a, span, tid);
+    __syncthreads();
+  }
   if (warp == 0) {
     int s, blk;
-    find_block(a, span, blockIdx.x, lane, s, blk);
+    find_block<C::kThreads>(a, span, blockIdx.x, lane, s_part, s, blk);
     if (lane == 0) {
       s_seq = s;
       s_blk = blk;

@@ -23,9 +23,13 @@
 namespace tq {
 namespace {
 
-constexpr int kTcMinRows = 16;   // rows of a group above which the tcgen05 prefix pass runs
-constexpr int kTcFixed = 4;
-constexpr int kSuffixFixed = 1;
+// Rows of a group above which the tcgen05 prefix pass runs.  One group, 8 KV
+// heads, 3/3 bits, the whole call, tcgen05 / 16-row tiles: 20 rows, 1024 shared
+// positions 18.6 / 20.7 us, 65536 70 / 87; 64 rows 20.2 / 28.9 and 73 / 159; 128
+// rows 23.8 / 30.8 and 82 / 366.
+constexpr int kTcMinRows = 16;
+constexpr int kTcFixed = 4;      // a tcgen05 CTA's prologue and partial, in tile times (8 us; a tile takes 2)
+constexpr int kSuffixFixed = 1;  // a CTA's prologue behind the prefix, in stages of 128 positions
 
 struct MergeArgs {
   DeviceParams p;
@@ -42,8 +46,8 @@ struct MergeArgs {
 // the split partials of one row, then every thread takes output coordinate
 // `tid` (and tid + 128 at d = 256) of all of them, so that a row of Pi^T is
 // loaded once for kMergeRows rows.  One row per CTA, as the merge of
-// tq_decode_attention has it, read Pi^T (32 KB) for every row: 21 us for 1024
-// rows of 25 partials where this takes 11.
+// tq_decode_attention has it, reads Pi^T (32 KB) for every row: 21 us for 1024
+// rows of 25 partials, where this takes 11.5 for 1024 rows of 19.
 constexpr int kMergeRows = 4;
 
 template <int DH>
@@ -150,9 +154,9 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
   s.nt_s = per > 8 ? 2 : 1;
   // The pass behind the prefix starts up to 63 positions before the prefix's
   // end.  Its units are many and short, so a split has to pay for its CTA's
-  // prologue (about kSuffixFixed stages of 128 positions): the count with the
-  // fewest stage times over all waves.  32 sequences of up to 1500 positions
-  // behind their prefix, 8 KV heads: 7 splits 30 us, 2 splits 20.
+  // prologue: the count with the fewest stage times over all waves.  32
+  // sequences of up to 1500 positions behind 32768 shared ones, 8 KV heads, the
+  // whole call: 1 split 78 us, 2 70, 3 (taken) 66, 4 69, 7 73.
   {
     const long stages = (max_suffix + 63 + 127) / 128, units = (long)n_seqs * n_kv_heads;
     const long slots = (long)sm_count() * shared_ctas_per_sm(d, bits_k, bits_v, qjl, s.nt_s);
