@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
         mx *= a.c;
         if (h == 0) {
           ref = fmaxf(mx, -3.0e38f);
-        } else if (__any_sync(0xffffffffu, mx > ref + kLazy)) {
+        } else if (__any_sync(0xffffffffu, pos >= 0 && mx > ref + kLazy)) {  // (rows of no query hold anything)
           // O is rescaled once the values of step h - 1 are in it: the scores of
           // step h + 1 were issued behind them (in front of the last step nothing
           // was, so those have a barrier of their own)

@@ -207,8 +207,8 @@ int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q
   args.members = plan.members;
   cfg.blockDim = dim3(kThreads);
   if (plan.p_splits > 0 && plan.tc) {
-    const SharedTcArgs t{p,         c,        n_q_heads,  q,            q_dtype,      scale,         cu_group, prefix,
-                         n_groups, max_group, max_prefix, plan.members, plan.p_chunk, args.partials, args.n_splits};
+    const SharedTcArgs t{p,      c,        n_q_heads, q,          q_dtype,      scale,        seq_lens,      cu_group,
+                         prefix, n_groups, max_group, max_prefix, plan.members, plan.p_chunk, args.partials, args.n_splits};
     cfg.gridDim = dim3(plan.p_splits, c.n_kv_heads, plan.units);
     const int e = launch_shared_prefix_tc(t, cfg);
     if (e != 0) return e;

@@ -164,12 +164,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // q's rows (bf16; fp32 q as hi + lo) into K~ of tile 1 (lo: of tile 0)
+  // q's rows (bf16; fp32 q as hi + lo) into K~ of tile 1 (lo: of tile 0); zero
+  // for members that take no part, whatever theirs hold: a moving reference
+  // rescales a warp's rows together
   const bool f32 = a.q_dtype == TQ_F32;
   for (int i = tid; i < 128 * 16; i += kTcThreads) {
     const int row = i >> 4, c = 8 * (i & 15);
     uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-    if (row < rows) {
+    if (row < rows && a.seq_lens[u.first + row / per] > 0) {
       const long at = ((long)(u.first + row / per) * a.n_q_heads + h * per + row % per) * D + c;
       if (f32) {
         const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at);

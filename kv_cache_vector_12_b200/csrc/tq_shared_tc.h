@@ -14,7 +14,7 @@ struct SharedTcArgs {
   const void *q;  // [n_seqs][n_q_heads][d], fp32 or bf16 (q_dtype)
   int q_dtype;
   float scale;
-  const int32_t *cu_group, *prefix;
+  const int32_t *seq_lens, *cu_group, *prefix;
   int n_groups, max_group, max_prefix;
   int members;       // sequences per CTA: 128 / (query heads per KV head)
   int chunk;         // positions per split, a multiple of 128

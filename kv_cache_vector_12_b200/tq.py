@@ -332,11 +332,13 @@ def build_tables(ctx: Context, cache: Cache, cached_lens: torch.Tensor, new_lens
     starts.  cu_group (int32 [n_groups + 1]) and prefix_lens (int32
     [n_groups]): groups of sequences that begin with the same blocks."""
     table = getattr(cache, "block_table", None)
-    _check(lib.tq_build_tables(ctx.handle, ctypes.byref(cache.struct), _ptr(table), _ptr(cached_lens),
-                               _ptr(new_lens), _ptr(free_list), 0 if free_list is None else free_list.numel(),
-                               _ptr(free_start), _ptr(free_end), _ptr(cu_group), _ptr(prefix_lens),
-                               0 if prefix_lens is None else prefix_lens.numel(), seq_idx.numel(), _ptr(seq_idx),
-                               _ptr(pos), _ptr(slots), _ptr(cu_new), _ptr(seq_lens), _stream(stream)))
+    p = [None if t is None else t.data_ptr()
+         for t in (table, cached_lens, new_lens, free_list, free_start, free_end, cu_group, prefix_lens, seq_idx, pos,
+                   slots, cu_new, seq_lens)]
+    _check(lib.tq_build_tables(ctx.handle, ctypes.byref(cache.struct), p[0], p[1], p[2], p[3],
+                               0 if free_list is None else free_list.numel(), p[4], p[5], p[6], p[7],
+                               0 if prefix_lens is None else prefix_lens.numel(), seq_idx.numel(), p[8], p[9], p[10],
+                               p[11], p[12], _stream(stream)))
 
 
 class WeightCache:

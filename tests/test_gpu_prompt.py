@@ -201,6 +201,25 @@ def test_same_call_twice_and_on_another_stream_and_captured(tq):
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [700, 1500])
+def test_same_bits_whatever_ran_before(tq, d, n):
+    """With 7 query heads a tile of 128 rows has two of no query, and the last tile more: what an earlier call left
+    in their place changes no bit."""
+    ctx = context(tq, d)
+    q, k, v = rows(n, 14, d, 1), rows(n, 2, d, 2), rows(n, 2, d, 3)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    outs = []
+    for mag in (0.0, 1.0, 300.0):
+        tq.prompt_attention(ctx, rows(n, 16, d, 9, mag), k, v, cu, n, torch.empty(n, 16, d, device="cuda"))
+        out, lse = torch.empty(n, 14, d, device="cuda"), torch.empty(n, 14, device="cuda")
+        tq.prompt_attention(ctx, q, k, v, cu, n, out, lse)
+        outs.append((out, lse))
+    ctx.check_device_errors()
+    for out, lse in outs[1:]:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
 def test_bounds_out_of_range_are_flagged(tq):
     ctx = context(tq, 128)
     q, k, v = rows(100, 2, 128, 1), rows(100, 1, 128, 2), rows(100, 1, 128, 3)

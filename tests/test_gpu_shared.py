@@ -270,6 +270,21 @@ def test_many_groups(tq):
     Batch(tq, groups, prefixes, lens, n_kv=1, per=2, seed=7).run()
 
 
+def test_queries_of_sequences_that_take_no_part_reach_nothing(tq):
+    """Length 0, and a query of NaN, infinity or zero: the others' outputs keep their bits."""
+    for n in (3, 40):
+        lens = [900 + (s % 9) if s % 3 else 0 for s in range(n)]
+        b, outs = Batch(tq, [0, n], [900], lens, seed=4), []
+        for x in (0.0, float("nan"), float("inf"), 1e4):
+            b.q[::3] = x
+            out, lse = b.call()
+            b.ctx.check_device_errors()
+            outs.append((out, lse))
+        b.check(*outs[1])
+        for out, lse in outs[1:]:
+            assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
 def test_equals_decode_attention_over_copies(tq):
     """The same values as tq_decode_attention where every sequence holds the prefix itself."""
     n, prefix, lens = 3, 640, [700, 641, 777]
