@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
   // per map (two for the slots) where they lie in one block of one sequence
   constexpr int kTokVec = VEC ? 4 : 1;
   const int rows = min(total_tok, a.n_tok);
-  const int stride = gridDim.x * kTabThreads;
+  const unsigned stride = gridDim.x * kTabThreads;  // (unsigned: an index past 2^31 - 1 ends its loop)
   auto slot_of = [&](int s, int c, int p) -> long {
     if (!paged) return (long)s * a.capacity + p;
     const int j = block_of(a, p), first = blocks_of(a, c);
@@ -172,10 +172,11 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
     return -1;
   };
 #pragma unroll 1
-  for (int r0 = kTokVec * (blockIdx.x * kTabThreads + tid); r0 < rows; r0 += kTokVec * stride) {
+  for (unsigned at = kTokVec * (blockIdx.x * kTabThreads + tid); at < (unsigned)rows; at += kTokVec * stride) {
+    const int r0 = (int)at;
     int s = last_at_most(s_tok, a.n_seqs, r0);
     const int c = s_c[s], p = c + (r0 - s_tok[s]);
-    if (VEC && r0 + kTokVec <= min(rows, s_tok[s + 1]) && block_of(a, p) == block_of(a, p + kTokVec - 1)) {
+    if (VEC && min(rows, s_tok[s + 1]) - r0 >= kTokVec && block_of(a, p) == block_of(a, p + kTokVec - 1)) {
       *reinterpret_cast<int4 *>(a.seq_idx + r0) = make_int4(s, s, s, s);
       *reinterpret_cast<int4 *>(a.pos + r0) = make_int4(p, p + 1, p + 2, p + 3);
       if (a.slots) {
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
       }
     } else {
 #pragma unroll 1
-      for (int r = r0; r < min(r0 + kTokVec, rows); ++r) {
+      for (int r = r0; r < r0 + min(kTokVec, rows - r0); ++r) {
         while (r >= s_tok[s + 1]) ++s;  // the next sequence with tokens
         const int q = s_c[s] + (r - s_tok[s]);
         a.seq_idx[r] = s;
@@ -197,8 +198,8 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
   if (!paged) return;
 
   // ---- new table entries, one per thread
-  for (int i = blockIdx.x * kTabThreads + tid; i < total_blk; i += stride) {
-    const int s = last_at_most(s_blk, a.n_seqs, i);
+  for (unsigned at = blockIdx.x * kTabThreads + tid; at < (unsigned)total_blk; at += stride) {
+    const int i = (int)at, s = last_at_most(s_blk, a.n_seqs, i);
     a.table[(long)s * a.per_seq + blocks_of(a, s_c[s]) + (i - s_blk[s])] = take_block(a, start, i);
   }
 

@@ -259,3 +259,25 @@ def test_step_captured_and_replayed_feeds_quantize(tq, ctx):
     for name in ("codes_k", "codes_v", "norm_k", "norm_v"):
         got = cache.planes[name][slots // bs, :, slots % bs]
         assert torch.equal(got, flat.planes[name][0].transpose(0, 1)[:n_tok]), name
+
+
+def test_the_most_tokens(tq, ctx):
+    """2^31 - 1 new tokens, an index short of what 32 bits hold: every row, and none past them."""
+    half = 2 ** 30
+    cache = tq.Cache(ctx, 2, 1, 64)
+    cache.struct.capacity = half  # (no plane is used)
+    n = 2 * half - 1
+    b = buffers(2, 0)
+    del b["free_end"]
+    b["slots"] = None
+    b["seq_idx"], b["pos"] = (torch.full((n + 1,), -7, dtype=torch.int32, device="cuda")[:n] for _ in range(2))
+    tq.build_tables(ctx, cache, dev([0, 0]), dev([half, half - 1]), **b)
+    ctx.check_device_errors()
+    assert b["cu_new"].tolist() == [0, half, n] and b["seq_lens"].tolist() == [half, half - 1]
+    for s, a, e in ((0, 0, half), (1, half, n)):
+        for i in range(a, e, 2 ** 27):
+            j = min(i + 2 ** 27, e)
+            assert (b["seq_idx"][i:j] == s).all()
+            assert torch.equal(b["pos"][i:j], torch.arange(i - a, j - a, dtype=torch.int32, device="cuda"))
+    for x in (b["seq_idx"], b["pos"]):
+        assert x.as_strided((1,), (1,), n).item() == -7
