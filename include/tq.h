@@ -359,9 +359,14 @@ size_t tq_shared_workspace_bytes(const tq_ctx *ctx, const tq_cache *cache,
  * used, whatever they hold (those from the prefix rounded down to a multiple
  * of 64 are read and masked).  In a paged cache a member's table is read from
  * the block that holds the prefix's end on, and only if it has positions
- * there; entries before it may hold anything.  A sequence outside every group,
- * in a group of more than max_group, or with lengths outside the bounds gets out = 0, lse = -inf and sets the
- * seq_len flag of tq_check_device_errors.
+ * there; entries before it may hold anything.  The first sequence's table has
+ * to hold the prefix only if some member takes part.  A sequence outside every
+ * group, in a group of more than max_group, or with lengths outside the bounds
+ * gets out = 0, lse = -inf and sets the seq_len flag of tq_check_device_errors.
+ * out, lse and the workspace may not overlap an input or one another.  The
+ * workspace holds nothing between calls: calls one behind the other may use the
+ * same one, calls (and replayed graphs) that may run at the same time each need
+ * their own.  A capacity of more than 2^30 is TQ_ERR_UNSUPPORTED.
  */
 tq_status tq_decode_attention_shared(
     tq_ctx *ctx, const tq_cache *cache, const void *q, int32_t q_dtype,
@@ -392,6 +397,7 @@ tq_status tq_decode_attention_shared(
  *  out         device [n_tok][n_q_heads][d] of out_dtype (TQ_BF16 or TQ_F32),
  *              lse device fp32 [n_tok][n_q_heads] or NULL.  Tokens outside
  *              every prompt are neither read for another's result nor written.
+ *              Neither may overlap an input.
  * scale <= 0 means 1/sqrt(d).  No workspace.  Query heads per KV head at most
  * 16.  Scores and sums are fp32; the softmax weights are rounded to bf16 for
  * the product with V.  A NaN or infinity in a token's K or V reaches, besides

@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <vector>
 
 #include "tq_internal.h"
@@ -128,10 +129,25 @@ tq_status check_geometry(const tq_cache *c) {
   return TQ_OK;
 }
 
-// Whether [a, a + na) and [b, b + nb) share a byte (a NULL pointer is no range).
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a && b && na && nb && x < y + nb && y < x + na;
+// A range of memory; a NULL pointer or no bytes: none.
+struct Range {
+  const void *p;
+  size_t bytes;
+};
+
+// Whether an output shares a byte with an input or with another output.
+bool clash(std::initializer_list<Range> out, std::initializer_list<Range> in) {
+  const auto meet = [](const Range &a, const Range &b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Range *o = out.begin(); o != out.end(); ++o) {
+    for (const Range &r : in)
+      if (meet(*o, r)) return true;
+    for (const Range *e = out.begin(); e != o; ++e)
+      if (meet(*o, *e)) return true;
+  }
+  return false;
 }
 
 tq_status check_cache(const tq_ctx *ctx, const tq_cache *c) {
@@ -594,6 +610,8 @@ tq_status check_shared_sizes(const tq_cache *cache, int32_t n_q_heads, int32_t n
     return fail(TQ_ERR_INVALID, "max_prefix_len=%d outside [0, capacity=%d]", max_prefix_len, cache->capacity);
   if (max_suffix_len < 0 || max_suffix_len > cache->capacity)
     return fail(TQ_ERR_INVALID, "max_suffix_len=%d outside [0, capacity=%d]", max_suffix_len, cache->capacity);
+  if (cache->capacity > 1 << 30)  // (the passes count positions past an end in 32 bits)
+    return fail(TQ_ERR_UNSUPPORTED, "capacity=%d > 2^30", cache->capacity);
   return TQ_OK;
 }
 
@@ -634,6 +652,13 @@ tq_status tq_decode_attention_shared(tq_ctx *ctx, const tq_cache *cache, const v
       ((uintptr_t)cu_group & 3u) || ((uintptr_t)prefix_lens & 3u) || (lse && ((uintptr_t)lse & 3u)))
     return fail(TQ_ERR_INVALID, "misaligned q/out (16 B), workspace (256 B) or seq_lens/cu_group/prefix_lens/lse (4 B)");
   if (!std::isfinite(scale)) return fail(TQ_ERR_INVALID, "scale is not finite");
+  const size_t rows = (size_t)cache->n_seqs * n_q_heads, elems = rows * ctx->d;
+  if (clash({{out, elems * (out_dtype == TQ_F32 ? 4 : 2)}, {lse, 4 * rows}, {workspace, workspace_bytes}},
+            {{q, elems * (q_dtype == TQ_F32 ? 4 : 2)},
+             {seq_lens, 4 * (size_t)cache->n_seqs},
+             {cu_group, 4 * ((size_t)n_groups + 1)},
+             {prefix_lens, 4 * (size_t)n_groups}}))
+    return fail(TQ_ERR_INVALID, "out, lse or the workspace overlaps another argument");
   const tq::SharedPlan plan =
       shared_plan(ctx, cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len);
   if (workspace_bytes < plan.workspace)
@@ -767,6 +792,16 @@ tq_status tq_prompt_attention(tq_ctx *ctx, const void *q, const void *k, const v
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || ((uintptr_t)cu_seqlens & 3u) ||
       (lse && ((uintptr_t)lse & 3u)))
     return fail(TQ_ERR_INVALID, "misaligned q/k/v/out (16 B) or cu_seqlens/lse (4 B)");
+  const auto bytes = [&](int64_t stride, int heads) {
+    return 2 * ((size_t)(n_tok - 1) * (size_t)stride + (size_t)heads * ctx->d);
+  };
+  const size_t out_rows = (size_t)n_tok * n_q_heads;
+  if (clash({{out, out_rows * ctx->d * (out_dtype == TQ_F32 ? 4 : 2)}, {lse, 4 * out_rows}},
+            {{q, bytes(q_stride, n_q_heads)},
+             {k, bytes(k_stride, n_kv_heads)},
+             {v, bytes(v_stride, n_kv_heads)},
+             {cu_seqlens, 4 * ((size_t)n_seqs + 1)}}))
+    return fail(TQ_ERR_INVALID, "out or lse overlaps another argument");
   if (scale <= 0.f) scale = 1.0f / std::sqrt((float)ctx->d);
   const int e = tq::launch_prompt(ctx->dp, q, k, v, (long)q_stride, (long)k_stride, (long)v_stride, n_tok, n_q_heads,
                                   n_kv_heads, cu_seqlens, n_seqs, max_len, scale, out, out_dtype == TQ_F32, lse,
@@ -806,32 +841,20 @@ tq_status tq_build_tables(tq_ctx *ctx, const tq_cache *cache, int32_t *block_tab
   if ((uintptr_t)slots & 7u) return fail(TQ_ERR_INVALID, "slots must be 8-byte aligned");
   // Every CTA reads the inputs on its own, so no output may lie over one.
   const size_t n = (size_t)cache->n_seqs;
-  struct Range {
-    const void *p;
-    size_t bytes;
-  };
-  const Range in[] = {{cached_lens, 4 * n},
-                      {new_lens, 4 * n},
-                      {block_table ? free_list : nullptr, 4 * (size_t)(n_free > 0 ? n_free : 0)},
-                      {block_table ? free_start : nullptr, 4},
-                      {n_groups ? cu_group : nullptr, 4 * ((size_t)n_groups + 1)},
-                      {n_groups ? prefix_lens : nullptr, 4 * (size_t)n_groups}};
-  const Range out[] = {{block_table, block_table ? 4 * n * (size_t)(cache->capacity / cache->block_size) : 0},
-                       {block_table ? free_end : nullptr, 4},
-                       {seq_idx, 4 * (size_t)n_tok},
-                       {pos, 4 * (size_t)n_tok},
-                       {slots, 8 * (size_t)n_tok},
-                       {cu_new, 4 * (n + 1)},
-                       {seq_lens, 4 * n}};
-  const int n_out = (int)(sizeof out / sizeof out[0]);
-  for (int i = 0; i < n_out; ++i) {
-    for (const Range &r : in)
-      if (overlap(out[i].p, out[i].bytes, r.p, r.bytes))
-        return fail(TQ_ERR_INVALID, "an output overlaps an input");
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
-        return fail(TQ_ERR_INVALID, "two outputs overlap");
-  }
+  if (clash({{block_table, block_table ? 4 * n * (size_t)(cache->capacity / cache->block_size) : 0},
+             {block_table ? free_end : nullptr, 4},
+             {seq_idx, 4 * (size_t)n_tok},
+             {pos, 4 * (size_t)n_tok},
+             {slots, 8 * (size_t)n_tok},
+             {cu_new, 4 * (n + 1)},
+             {seq_lens, 4 * n}},
+            {{cached_lens, 4 * n},
+             {new_lens, 4 * n},
+             {block_table ? free_list : nullptr, 4 * (size_t)(n_free > 0 ? n_free : 0)},
+             {block_table ? free_start : nullptr, 4},
+             {n_groups ? cu_group : nullptr, 4 * ((size_t)n_groups + 1)},
+             {n_groups ? prefix_lens : nullptr, 4 * (size_t)n_groups}}))
+    return fail(TQ_ERR_INVALID, "an output overlaps an input or another output");
   const int e = tq::launch_tables(ctx->dp, *cache, block_table, cached_lens, new_lens, free_list, n_free, free_start,
                                   free_end, cu_group, prefix_lens, n_groups, n_tok, seq_idx, pos, slots, cu_new,
                                   seq_lens, stream);

@@ -325,6 +325,7 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
       u = find_members(a.cu_group, a.n_groups, a.max_group, a.members, a.c.n_seqs, blockIdx.z, lane);
       if (u.count == 0) return;
       const int len = a.prefix[u.group];
+      if (!any_member(a.seq_lens, u, lane)) return;
       // (a prefix outside its bounds is flagged by the other pass)
       if (len <= 0 || len > a.max_prefix || len > a.c.capacity) return;
       s = u.lead;

@@ -52,6 +52,14 @@ __device__ __forceinline__ SharedUnit find_members(const int32_t *cu, int n_grou
   return u;
 }
 
+// Whether a member of the unit takes part.  A unit of finished sequences has no
+// work, and its table rows may hold anything.
+__device__ __forceinline__ bool any_member(const int32_t *seq_lens, const SharedUnit &u, int lane) {
+  bool any = false;
+  for (int i = lane; i < u.count; i += 32) any |= seq_lens[u.first + i] > 0;
+  return __any_sync(0xffffffffu, any);
+}
+
 // What sequence s attends over: its group's prefix [0, prefix) and its own
 // [prefix, len).  Length 0: no part.  bad: outside every group, or its group or
 // lengths outside the call's bounds; its len and prefix are then 0.

@@ -50,6 +50,7 @@ constexpr int kSmallLen64 = 2048, kSmallLen128 = 768;
 constexpr int kStep = 64;     // keys per step: one S buffer
 constexpr int kPoly = 4;      // pairs of every 16 whose exp2 runs on the FMA pipe
 constexpr float kLazy = 8.f;  // log2 units a tile's maximum may pass the reference
+constexpr float kFloor = -3.0e38f;  // of the reference: a difference to it is never inf - inf
 
 // Two forms.  With two row tiles (d = 64 and 128) a CTA fills an SM and shares
 // K and V between them: long prompts.  With one row tile, tiles of 64 keys and
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
           for (int e = 0; e < 32; e += 2) mx = max3(mx, f(v[c][e]), f(v[c][e + 1]));
         mx *= a.c;
         if (h == 0) {
-          ref = fmaxf(mx, -3.0e38f);
+          ref = fmaxf(mx, kFloor);
         } else if (__any_sync(0xffffffffu, pos >= 0 && mx > ref + kLazy)) {  // (rows of no query hold anything)
           // O is rescaled once the values of step h - 1 are in it: the scores of
           // step h + 1 were issued behind them (in front of the last step nothing
@@ -517,7 +518,11 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
         ok = warp_wait(&o_full[i], 0, a.err, &stop);
         if (ok) {
           tc_fence_after();
-          const float il = 1.f / l;
+          // A row whose scores are all -inf (its reference never moved off the
+          // floor) has no weights but what the polynomial puts for 2^-inf:
+          // o = 0 / 0 and lse = -inf, or NaN where a score was one
+          if (!(ref > kFloor)) l *= 0.f;
+          const float il = l > 0.f ? 1.f / l : __int_as_float(0x7fc00000);
           const long orow = pos < 0 ? 0 : (long)(tok0 + pos) * a.n_q_heads + h_kv * G + row % G;
 #pragma unroll 1
           for (int c = 0; c < DH / 32; ++c) {
@@ -591,11 +596,13 @@ int launch(PromptArgs args, const void *q, const void *k, const void *v, long qs
   // at most this many query blocks, whatever the lengths
   const long span = (long)C::NT * args.per_tile;
   const long by_tok = (long)args.n_tok / span + args.n_seqs, by_len = (args.max_len + span - 1) / span * args.n_seqs;
+  const long ctas = by_tok < by_len ? by_tok : by_len;
+  if (ctas > 0x7fffffffl) return (int)cudaErrorInvalidConfiguration;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(by_tok < by_len ? by_tok : by_len), args.n_kv_heads);
+  cfg.gridDim = dim3((unsigned)ctas, args.n_kv_heads);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::smem;
   cfg.stream = (cudaStream_t)stream;

@@ -129,7 +129,8 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
   s.members = (s.tc ? 128 : 8 * s.nt_p) / per;
   const long by_group = (long)n_groups * ((max_group + s.members - 1) / s.members);
   const long by_seq = (long)n_seqs / s.members + n_groups;
-  s.units = (int)(by_group < by_seq ? by_group : by_seq);
+  const long most = by_group < by_seq ? by_group : by_seq;
+  s.units = (int)(most < n_seqs ? most : n_seqs);  // (a unit holds a sequence)
   if (max_prefix > 0 && s.tc) {
     // splits of whole 128-key tiles, one CTA per SM: the count with the fewest
     // tile times over all waves, kTcFixed of them per CTA for its prologue

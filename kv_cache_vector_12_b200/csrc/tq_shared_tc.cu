@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
   const SharedUnit u = find_members(a.cu_group, a.n_groups, a.max_group, a.members, a.c.n_seqs, blockIdx.z, lane);
   if (u.count == 0) return;
   const int prefix = a.prefix[u.group];
+  if (!any_member(a.seq_lens, u, lane)) return;
   // (a prefix outside its bounds is flagged by the pass behind it)
   if (prefix <= 0 || prefix > a.max_prefix || prefix > a.c.capacity) return;
   const int t0 = split * a.chunk;

@@ -313,10 +313,16 @@ def prompt_attention(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Te
     n_q_heads, d], k and v bf16 [n_tok, n_kv_heads, d] (slices of one fused
     projection are taken by their token stride); out bf16 or fp32 [n_tok,
     n_q_heads, d], lse fp32 [n_tok, n_q_heads]."""
-    out_dtype = TQ_F32 if out.dtype == torch.float32 else TQ_BF16
-    _check(lib.tq_prompt_attention(ctx.handle, _ptr(q), _ptr(k), _ptr(v), q.stride(0), k.stride(0), v.stride(0),
-                                   q.shape[0], q.shape[1], k.shape[1], _ptr(cu_seqlens), cu_seqlens.numel() - 1,
-                                   max_len, scale, _ptr(out), out_dtype, _ptr(lse), _stream(stream)))
+    n_tok, n_q_heads, d = q.shape
+    (q0, q1, q2), (k0, k1, k2), (v0, v1, v2) = q.stride(), k.stride(), v.stride()
+    if not (q.dtype is k.dtype is v.dtype is torch.bfloat16 and q1 == k1 == v1 == d == ctx.d and q2 == k2 == v2 == 1
+            and out.is_contiguous()):
+        raise TQError(TQ_ERR_INVALID, "prompt_attention takes bf16 q, k, v with the heads of a token contiguous, "
+                                      "and a contiguous out")
+    out_dtype = TQ_F32 if out.dtype is torch.float32 else TQ_BF16
+    _check(lib.tq_prompt_attention(ctx.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, k0, v0, n_tok, n_q_heads,
+                                   k.shape[1], _ptr(cu_seqlens), cu_seqlens.numel() - 1, max_len, scale,
+                                   out.data_ptr(), out_dtype, _ptr(lse), _stream(stream)))
 
 
 def build_tables(ctx: Context, cache: Cache, cached_lens: torch.Tensor, new_lens: torch.Tensor, seq_idx: torch.Tensor,

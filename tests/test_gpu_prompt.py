@@ -261,3 +261,67 @@ def test_refusals_and_empty_calls(tq):
     tq.prompt_attention(ctx, q, k, v, torch.zeros(4, dtype=torch.int32, device="cuda"), 64, out)  # three empty ones
     ctx.check_device_errors()
     assert (out == 7.0).all()
+
+
+def test_refused_layouts_and_overlaps(tq):
+    """What the strides or the types cannot say, and outputs over an input."""
+    ctx = context(tq, 128)
+    q, k, v = rows(64, 4, 128, 1), rows(64, 2, 128, 2), rows(64, 2, 128, 3)
+    cu = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((64, 4), 7.0, device="cuda")
+    kept = [t.clone() for t in (q, k, v)]
+
+    def refused(**kw):
+        with pytest.raises(tq.TQError) as ei:
+            tq.prompt_attention(ctx, **{**dict(q=q, k=k, v=v, cu_seqlens=cu, max_len=64, out=out, lse=lse), **kw})
+        assert ei.value.status == tq.TQ_ERR_INVALID
+
+    refused(q=q.float())
+    refused(k=k.half())
+    refused(v=rows(64, 4, 128, 3)[:, ::2])              # every second head
+    refused(k=rows(2, 64, 128, 2).transpose(0, 1))      # heads first
+    refused(q=rows(64, 4, 64, 1))                       # another head dimension
+    refused(out=torch.empty(4, 64, 128, device="cuda").transpose(0, 1))
+    refused(out=q)
+    whole = torch.zeros(64 * 512 + 64, dtype=torch.bfloat16, device="cuda")
+    refused(q=whole[:64 * 512].view(64, 4, 128), out=whole[64:].view(64, 4, 128))
+    refused(lse=k.view(-1).view(torch.float32)[:256].view(64, 4))
+    refused(lse=out.view(-1).view(torch.float32)[-256:].view(64, 4))
+    ctx.check_device_errors()
+    assert (out == 7.0).all() and (lse == 7.0).all() and all(torch.equal(a, b) for a, b in zip(kept, (q, k, v)))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_whose_scores_are_all_minus_infinity(tq, d):
+    """softmax of nothing but -inf: NaN and lse = -inf as by the formula; a row
+    with one finite score gets that key's value."""
+    ctx, n = context(tq, d), 300
+    q, k, v = rows(n, 2, d, 1), rows(n, 1, d, 2), rows(n, 1, d, 3)
+    q[:, :, 0], k[:, :, 0] = 1.0, -math.inf
+    k[250] = 0.0
+    out, lse = torch.empty(n, 2, d, device="cuda"), torch.empty(n, 2, device="cuda")
+    tq.prompt_attention(ctx, q, k, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"), n, out, lse)
+    ctx.check_device_errors()
+    assert out[:250].isnan().all() and (lse[:250] == -math.inf).all()
+    # That key's weight is 2^0, which either exp2 gives within 2^-22; rounded to bf16 (steps of 2^-8 and 2^-7 around 1)
+    # it is 1, the others are at most 2^-126.  The sum keeps the 2^-22, so o = v / l and lse = ln l are off by at most
+    # that and fp32's roundings of 2^-24 each (reciprocal, product; log2, product): together below 2^-21.
+    ref = v[250].float().expand(n - 250, 2, d)
+    assert ((out[250:] - ref).abs() <= 2.0 ** -21 * ref.abs()).all() and (lse[250:].abs() <= 2.0 ** -21).all()
+
+
+def test_two_calls_at_once(tq):
+    """On two streams, with nothing shared but the context and the inputs."""
+    ctx, lens = context(tq, 128), [700, 1, 333, 64]
+    n = sum(lens)
+    q, k, v = rows(n, 8, 128, 1), rows(n, 2, 128, 2), rows(n, 2, 128, 3)
+    cu = torch.tensor([0, 700, 701, 1034, n], dtype=torch.int32, device="cuda")
+    ref = torch.empty(n, 8, 128, dtype=torch.bfloat16, device="cuda")
+    tq.prompt_attention(ctx, q, k, v, cu, 700, ref)
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [torch.zeros_like(ref) for _ in range(20)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        tq.prompt_attention(ctx, q, k, v, cu, 700, o, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    ctx.check_device_errors()
+    assert all(torch.equal(o, ref) for o in outs)

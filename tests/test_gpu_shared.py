@@ -383,3 +383,65 @@ def test_refusals(tq):
     assert tq.shared_workspace_bytes(b.ctx, b.cache, 7, 1, 2, 64, 64) == 0
     b.ctx.check_device_errors()
     assert (ok["out"] == 7.0).all()
+
+
+@pytest.mark.parametrize("d,qjl,n", [(128, 0, 6), (128, 0, 2), (64, 0, 3), (128, 1, 4)])
+def test_a_finished_group_holds_nothing(tq, d, qjl, n):
+    """A padded batch: no member of the group takes part, so its table rows may name no block."""
+    b = Batch(tq, [0, n, n + 3], [200, 130], [0] * n + [200, 130, 190], d=d, qjl=qjl, block=64, per=4)
+    b.cache.block_table[:n] = -1
+    out, lse = b.call()
+    b.ctx.check_device_errors()
+    b.check(out, lse)
+
+
+def test_one_member_groups_fill_the_batch(tq):
+    """As many groups as sequences, with room for more members than any has: units are counted by sequences."""
+    n = 300
+    Batch(tq, list(range(n + 1)), [65 + s % 3 for s in range(n)], [70 + s % 7 for s in range(n)], n_kv=1, per=16).run(
+        max_group=n)
+
+
+def test_refused_overlaps_and_capacity(tq):
+    b = Batch(tq, [0, 2], [64], [80, 90])
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = tq.alloc_shared_workspace(b.ctx, b.cache, 8, 1, 2, 64, 64)
+    ok = dict(q=b.q, seq_lens=ints([80, 90]), cu_group=ints([0, 2]), prefix_lens=ints([64]), max_group=2,
+              max_prefix_len=64, max_suffix_len=64, out=torch.full(b.q.shape, 7.0, device="cuda"),
+              lse=torch.full(b.q.shape[:2], 7.0, device="cuda"), workspace=ws)
+    kept = b.q.clone()
+
+    def refused(status=tq.TQ_ERR_INVALID, **kw):
+        with pytest.raises(tq.TQError) as ei:
+            tq.decode_attention_shared(b.ctx, b.cache, **{**ok, **kw})
+        assert ei.value.status == status
+
+    refused(out=b.q)
+    refused(lse=ok["out"].view(-1)[:16].view(2, 8))
+    refused(out=ws.view(torch.float32)[:b.q.numel()].view(b.q.shape))
+    refused(seq_lens=ws[256:264].view(torch.int32))
+    refused(lse=b.q.view(-1)[-16:].view(2, 8))
+    capacity = b.cache.struct.capacity
+    b.cache.struct.capacity = 2 ** 30 + 64
+    refused(status=tq.TQ_ERR_UNSUPPORTED)
+    assert tq.shared_workspace_bytes(b.ctx, b.cache, 8, 1, 2, 64, 64) == 0
+    b.cache.struct.capacity = capacity
+    b.ctx.check_device_errors()
+    assert (ok["out"] == 7.0).all() and (ok["lse"] == 7.0).all() and torch.equal(b.q, kept)
+
+
+@pytest.mark.parametrize("n,per", [(3, 4), (40, 4)])
+def test_two_calls_at_once(tq, n, per):
+    """On two streams, each with its own workspace."""
+    b = Batch(tq, [0, n], [900], [901 + s % 60 for s in range(n)], per=per)
+    ref, ref_lse = b.call()
+    spaces = [tq.alloc_shared_workspace(b.ctx, b.cache, b.n_kv * per, 1, n, 900, 60) for _ in range(2)]
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [torch.zeros_like(ref) for _ in range(20)]
+    ints = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (b.lens, b.groups, b.prefixes)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        tq.decode_attention_shared(b.ctx, b.cache, b.q, *ints, n, 900, 60, o, None, spaces[i % 2],
+                                   stream=streams[i % 2])
+    torch.cuda.synchronize()
+    b.ctx.check_device_errors()
+    assert all(torch.equal(o, ref) for o in outs)
