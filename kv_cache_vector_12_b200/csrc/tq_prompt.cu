@@ -68,15 +68,22 @@ struct PromptCfg {
   static constexpr int kKVBox = KT * 128;           // bytes of one box of a K or V tile
   static constexpr int kQTile = kBoxes * kQBox;
   static constexpr int kSlot = kBoxes * kKVBox;
-  static constexpr int kSlots = DH == 64 ? (NT == 2 ? 8 : 5) : DH == 128 && NT == 1 ? 4 : 5;  // at least 4
+  // Q goes to tensor memory where that has room for it (d = 256): through the
+  // ring's first kQItems slots, so that K and V have 7 slots instead of 5
+  static constexpr bool kQTmem = DH == 256;
+  static constexpr int kQItems = kQTmem ? kQTile / kSlot : 0;
+  static constexpr int kSlots = DH == 64 ? (NT == 2 ? 8 : 5) : DH == 128 ? (NT == 1 ? 4 : 5) : 7;  // at least 4
   static constexpr int kSoftWarps = 4 * NT;
   static constexpr int kProdWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
   static constexpr int kThreads = 32 * (kSoftWarps + 1 + NT);  // an MMA warp per row tile
-  static constexpr int smem = 1024 + NT * kQTile + kSlots * kSlot;
-  // tensor-memory columns: two S buffers per row tile (P over them) and O
+  static constexpr int kQBytes = kQTmem ? 0 : NT * kQTile;
+  static constexpr int smem = 1024 + kQBytes + kSlots * kSlot;
+  // tensor-memory columns: two S buffers per row tile (P over them), O, and Q at d = 256
   static constexpr uint32_t kCols = NT * (128u + DH) <= 256 ? 256 : 512;
   static constexpr uint32_t s_col(int i, int b) { return 128u * i + 64u * b; }
   static constexpr uint32_t o_col(int i) { return 128u * NT + (uint32_t)DH * i; }
+  static constexpr uint32_t q_col = (128u + DH) * NT;
+  static_assert(!kQTmem || (NT == 1 && q_col + DH / 2 <= kCols && kQTile % kSlot == 0), "room for Q");
   // instruction descriptors, kind::f16: bf16 A and B, fp32 D, M = 128; S has
   // both operands K-major, O has B MN-major (bit 16)
   static constexpr uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
   constexpr int NT = C::NT, KT = C::KT;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  unsigned char *ring = sm + NT * C::kQTile;
+  unsigned char *ring = sm + C::kQBytes;
   __shared__ __align__(8) uint64_t q_full, full[C::kSlots], empty[C::kSlots];
   __shared__ __align__(8) uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], fin[2];  // [row tile][buffer]
   __shared__ uint32_t tmem_slot;
@@ -281,7 +288,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == C::kProdWarp && lane == 0) {
-    bar_init(smem_addr(&q_full), 1);
+    bar_init(smem_addr(&q_full), C::kQTmem ? 4 : 1);  // (in tensor memory: by the softmax warps)
     for (int i = 0; i < C::kSlots; ++i) {
       bar_init(smem_addr(&full[i]), 1);
       bar_init(smem_addr(&empty[i]), NT);
@@ -321,21 +328,22 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
       // ---------------- producer
       if (lane == 0) {
         const uint32_t box = (uint32_t)(PC * G * 128);
-        bar_expect_tx(smem_addr(&q_full), (NT == 2 && steps[1] ? 2 : 1) * C::kBoxes * box);
+        if (!C::kQTmem) bar_expect_tx(smem_addr(&q_full), (NT == 2 && steps[1] ? 2 : 1) * C::kBoxes * box);
+        for (int i = 0; i < C::kQItems; ++i) bar_expect_tx(smem_addr(&full[i]), C::kBoxes / C::kQItems * box);
         for (int i = 0; i < NT; ++i)
           if (steps[i])
-            for (int b = 0; b < C::kBoxes; ++b)
+            for (int b = 0; b < C::kBoxes; ++b)  // (in the ring: a slot after the other)
               tma_load_3d(smem_addr(sm + i * C::kQTile + b * C::kQBox), &map_q, 64 * b, h_kv * G, tok0 + first + i * PC,
-                          smem_addr(&q_full));
-        int issued = 0;
-        int slot = 0, phase = 1;
-        for (int it = 0; it < 2 * n_tiles; ++it) {  // K 0, V 0, K 1, V 1, ...
+                          smem_addr(C::kQTmem ? &full[b * C::kQBox / C::kSlot] : &q_full));
+        int issued = C::kQItems;
+        int slot = C::kQItems, phase = 1;
+        for (int it = C::kQItems; it < C::kQItems + 2 * n_tiles; ++it) {  // K 0, V 0, K 1, V 1, ...
           if (it >= C::kSlots && !wait_or_stop(&empty[slot], phase, a.err, &stop)) break;
           if (*(volatile int *)&stop) break;
           bar_expect_tx(smem_addr(&full[slot]), C::kSlot);
           for (int b = 0; b < C::kBoxes; ++b)
             tma_load_3d(smem_addr(ring + slot * C::kSlot + b * C::kKVBox), (it & 1) ? &map_v : &map_k, 64 * b, h_kv,
-                        tok0 + (it >> 1) * KT, smem_addr(&full[slot]));
+                        tok0 + ((it - C::kQItems) >> 1) * KT, smem_addr(&full[slot]));
           issued = it + 1;
           if (++slot == C::kSlots) {
             slot = 0;
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
           }
         }
         if (*(volatile int *)&stop) {  // never leave copies in flight
-          bar_wait(smem_addr(&q_full), 0);
+          if (!C::kQTmem) bar_wait(smem_addr(&q_full), 0);
           for (int it = max(0, issued - C::kSlots); it < issued; ++it)
             bar_wait(smem_addr(&full[it % C::kSlots]), (it / C::kSlots) & 1);
         }
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
       const int i = warp - C::kMmaWarp, mine = steps[i];
       // K tile of the step whose scores are next and V tile of the step whose
       // values are next: ring slots and their phases, advanced without division
-      int ks = 0, kp = 0, vs = 1, vp = 0;
+      int ks = C::kQItems, kp = 0, vs = C::kQItems + 1, vp = 0;
       auto advance = [&](int &slot, int &phase) {
         slot += 2;
         if (slot >= C::kSlots) {
@@ -372,6 +380,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
       // thread run in order); two S go ahead.  A tile's slot is given back after
       // its last step, also by a row tile that needs fewer.
       bool ok = warp_wait(&q_full, 0, a.err, &stop);
+      if (lane < C::kQItems && ok) bar_arrive(smem_addr(&empty[lane]));  // (Q's slots, read by the softmax warps)
       const int last = n_tiles * C::kSteps;
 #pragma unroll 1
       for (int h = -2; ok && h < last; ++h) {
@@ -396,8 +405,12 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
             const uint64_t k = k0 + (uint64_t)(ks * kSlotU + (n % C::kSteps) * kStepU);
 #pragma unroll
             for (int kk = 0; kk < DH / 16; ++kk)
-              tc_mma_n(d_s + 64u * (n & 1), q + (((kk >> 2) * C::kQBox + (kk & 3) * 32) >> 4),
-                       k + (((kk >> 2) * C::kKVBox + (kk & 3) * 32) >> 4), C::idesc_s, kk > 0);
+              if (C::kQTmem)
+                mma_ts(d_s + 64u * (n & 1), tmem + C::q_col + 8 * kk, k + (((kk >> 2) * C::kKVBox + (kk & 3) * 32) >> 4),
+                       C::idesc_s, kk > 0);
+              else
+                tc_mma_n(d_s + 64u * (n & 1), q + (((kk >> 2) * C::kQBox + (kk & 3) * 32) >> 4),
+                         k + (((kk >> 2) * C::kKVBox + (kk & 3) * 32) >> 4), C::idesc_s, kk > 0);
             tc_commit(smem_addr(&s_full[i][n & 1]));
           }
           if (k_end) tc_commit(smem_addr(&empty[ks]));
@@ -419,8 +432,30 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
       const uint32_t t_o = tmem + C::o_col(i) + lanes;
       float ref = 0.f, l = 0.f;
       bool ok = true;
+      if constexpr (C::kQTmem) {
+        // Q's row from the swizzled boxes into tensor memory, as the scores' A operand
 #pragma unroll 1
-      for (int h = 0; h < n; ++h) {
+        for (int b = 0; ok && b < C::kBoxes; ++b) {
+          if (b * C::kQBox % C::kSlot == 0) ok = warp_wait(&full[b * C::kQBox / C::kSlot], 0, a.err, &stop);
+          if (!ok) break;
+          uint32_t x[32];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(sm + b * C::kQBox + 128 * row + 16 * (e ^ (row & 7)));
+            x[4 * e] = u.x;
+            x[4 * e + 1] = u.y;
+            x[4 * e + 2] = u.z;
+            x[4 * e + 3] = u.w;
+          }
+          tmem_st32(tmem + C::q_col + lanes + 32 * b, x);
+        }
+        st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) bar_arrive(smem_addr(&q_full));
+      }
+#pragma unroll 1
+      for (int h = 0; ok && h < n; ++h) {
         const uint32_t t_s = tmem + C::s_col(i, h & 1) + lanes;
         ok = warp_wait(&s_full[i][h & 1], (h >> 1) & 1, a.err, &stop);
         if (!ok) break;
@@ -500,7 +535,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
         if (key0 + kStep > len) {
           // the step's rows behind the sequence's end hold other tokens: zero
           // them, so that a weight of 0 times what they hold stays 0
-          const int vs = 2 * (h / C::kSteps) + 1;
+          const int vs = C::kQItems + 2 * (h / C::kSteps) + 1;
           ok = warp_wait(&full[vs % C::kSlots], (vs / C::kSlots) & 1, a.err, &stop);
           if (!ok) break;
           unsigned char *vt = ring + (vs % C::kSlots) * C::kSlot + (h % C::kSteps) * (kStep * 128);
