@@ -29,7 +29,7 @@ namespace {
 // rows 23.8 / 30.8 and 82 / 366.
 constexpr int kTcMinRows = 16;
 constexpr int kTcFixed = 4;      // a tcgen05 CTA's prologue and partial, in tile times (8 us; a tile takes 2)
-constexpr int kSuffixFixed = 1;  // a CTA's prologue behind the prefix, in stages of 128 positions
+constexpr int kSuffixFixed = 1;  // a CTA's prologue in the 16-row passes, in stages of 128 positions
 
 struct MergeArgs {
   DeviceParams p;
@@ -128,9 +128,9 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
   s.nt_p = (long)per * max_group > 8 ? 2 : 1;
   s.members = (s.tc ? 128 : 8 * s.nt_p) / per;
   const long by_group = (long)n_groups * ((max_group + s.members - 1) / s.members);
-  const long by_seq = (long)n_seqs / s.members + n_groups;
-  const long most = by_group < by_seq ? by_group : by_seq;
-  s.units = (int)(most < n_seqs ? most : n_seqs);  // (a unit holds a sequence)
+  // sum ceil(c / m) <= sum (c + m - 1) / m over the groups' sizes c
+  const long by_seq = ((long)n_seqs + (long)n_groups * (s.members - 1)) / s.members;
+  s.units = (int)(by_group < by_seq ? by_group : by_seq);
   if (max_prefix > 0 && s.tc) {
     // splits of whole 128-key tiles, one CTA per SM: the count with the fewest
     // tile times over all waves, kTcFixed of them per CTA for its prologue
@@ -147,10 +147,25 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
       }
     }
   } else if (max_prefix > 0) {
-    const DecodeSplit sp =
-        decode_split(s.units, n_kv_heads, max_prefix, shared_ctas_per_sm(d, bits_k, bits_v, qjl, s.nt_p));
-    s.p_chunk = sp.chunk;
-    s.p_splits = sp.n_splits;
+    // the count with the fewest stage times over all waves, counted in halves of
+    // a stage, and a tenth of one for each split (its CTA's prologue beside
+    // others, and the merge).  Whole calls, 3/3 bits, 8 KV heads, 16 rows: 8192
+    // shared positions, 18 splits 30 us, 24 28, 43 32, 64 40; 65536, 36 splits 75,
+    // 55 60, 74 (two waves) 76; 16 groups of 4096, 2 splits 85, 3 72, 4 86.  With
+    // QJL the prologue has a second product (128 rows, 16384: 4 splits 188, 8 201).
+    const long fixed = qjl ? 3 : kSuffixFixed;
+    const long halves = (max_prefix + 63) / 64, lanes = (long)s.units * n_kv_heads;
+    const long slots = (long)sm_count() * shared_ctas_per_sm(d, bits_k, bits_v, qjl, s.nt_p);
+    long best = -1;
+    for (long n = 1; n <= halves && n <= 128; ++n) {
+      const long per_split = (halves + n - 1) / n, used = (halves + per_split - 1) / per_split;
+      const long cost = 5 * ((lanes * used + slots - 1) / slots * (per_split + 2 * fixed)) + used;
+      if (best < 0 || cost < best) {
+        best = cost;
+        s.p_chunk = (int)(per_split * 64);
+        s.p_splits = (int)used;
+      }
+    }
   }
   s.nt_s = per > 8 ? 2 : 1;
   // The pass behind the prefix starts up to 63 positions before the prefix's
