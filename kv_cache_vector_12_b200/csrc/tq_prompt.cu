@@ -28,7 +28,15 @@
 // kernel (one exp2 per score), do not wait for an MMA.  (With one buffer of
 // 128 keys a row tile alternated between 2000 cycles of softmax and 2100 of
 // hand-over and MMAs.)  Two row tiles per CTA at d = 64 and 128, one at d = 256,
-// where O alone takes half of tensor memory.
+// where O alone takes half of tensor memory; Q has the room that is left there,
+// so that the scores' A operand takes no shared-memory reads (32 cycles an MMA
+// of N = 64 instead of 50) and the ring has 7 slots instead of 5 (a K tile's load
+// no longer waits for the values of the step before): 540 -> 438 us for 5 prompts
+// of up to 5000 tokens, 16 over 4 heads.
+// Measured: one prompt of 32768 tokens, 32 over 8 heads, d = 128, 7.6 to 7.9 ms
+// (1.11 to 1.16 PFLOP/s, a plain bf16 GEMM sustains 1.40); 17 of up to 4001 tokens
+// 1.23 ms (1.0).  No pipe is full (tensor 49 %, MUFU 37 %, issue 42 %): what bounds
+// it are the hand-overs between the softmax and MMA warps of a row tile.
 // P is rounded to bf16, V's type (one MMA takes one type for A and B); l is
 // summed in fp32 from the unrounded weights.
 #include <cuda_bf16.h>
@@ -44,8 +52,8 @@ namespace {
 
 // longest prompt up to which the form with one row tile runs.  Measured, 32768
 // tokens of prompts of 1 .. n tokens, 8 KV and 32 query heads, one row tile / two:
-// d = 64, n = 256 107 / 136 us, 1024 157 / 172, 2048 229 / 229, 4096 452 / 428;
-// d = 128, n = 256 138 / 174, 512 170 / 190, 1024 212 / 210, 4096 640 / 452.
+// d = 64, n = 256 116 / 146 us, 1024 160 / 173, 2048 232 / 231, 4096 455 / 430;
+// d = 128, n = 256 144 / 181, 512 181 / 201, 1024 215 / 211, 4096 645 / 456.
 constexpr int kSmallLen64 = 2048, kSmallLen128 = 768;
 constexpr int kStep = 64;     // keys per step: one S buffer
 constexpr int kPoly = 4;      // pairs of every 16 whose exp2 runs on the FMA pipe
@@ -345,7 +353,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
       if (lane == 0) {
         const uint32_t box = (uint32_t)(PC * G * 128);
         if (!C::kQTmem) bar_expect_tx(smem_addr(&q_full), (NT == 2 && steps[1] ? 2 : 1) * C::kBoxes * box);
-        for (int i = 0; i < C::kQItems; ++i) bar_expect_tx(smem_addr(&full[i]), C::kBoxes / C::kQItems * box);
+        for (int i = 0; i < C::kQItems; ++i) bar_expect_tx(smem_addr(&full[i]), C::kSlot / C::kQBox * box);
         for (int i = 0; i < NT; ++i)
           if (steps[i])
             for (int b = 0; b < C::kBoxes; ++b)  // (in the ring: a slot after the other)

@@ -24,9 +24,9 @@ namespace tq {
 namespace {
 
 // Rows of a group above which the tcgen05 prefix pass runs.  One group, 8 KV
-// heads, 3/3 bits, the whole call, tcgen05 / 16-row tiles: 20 rows, 1024 shared
-// positions 18.6 / 20.7 us, 65536 70 / 87; 64 rows 20.2 / 28.9 and 73 / 159; 128
-// rows 23.8 / 30.8 and 82 / 366.
+// heads, 3/3 bits, the whole call, tcgen05 / 16-row tiles: 16 rows, 8192 shared
+// positions 27 / 29 us, 65536 73 / 62; 20 rows 25 / 32 and 73 / 88; 64 rows 31 / 44
+// and 75 / 160; 128 rows 39 / 65 and 86 / 305.
 constexpr int kTcMinRows = 16;
 constexpr int kTcFixed = 4;      // a tcgen05 CTA's prologue and partial, in tile times (8 us; a tile takes 2)
 constexpr int kSuffixFixed = 1;  // a CTA's prologue in the 16-row passes, in stages of 128 positions

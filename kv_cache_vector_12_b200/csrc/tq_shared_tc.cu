@@ -28,6 +28,10 @@
 // expanded once for 128 rows.  Why loops that are not unrolled: with every
 // loop unrolled (90 KB of code for five kinds of warps) instruction fetch took
 // two thirds of the time.
+// Measured, 3/3 bits, 8 KV heads: 128 rows behind 32768 positions 50 us (the
+// 16-row tiles 130), 32 rows behind 131008 123 us.  No pipe is full (tensor 29 %,
+// ALU 41 %, issue 55 %): a tile of 128 keys takes about 3700 cycles through the
+// hand-overs between the roles.
 #include <atomic>
 #include <cmath>
 
