@@ -85,8 +85,8 @@ struct DecodeVariant {
 // budget (its callers decode batches of many sequences).  At d = 256 every
 // build runs the 168-register budget (twice the value accumulators), at
 // d = 64 the 128-register one; kShort and kLong are then the same kernel.
-// kShared: the budget of kPaged, either layout, for batches whose groups share
-// a prefix.
+// kShared: the budget of kPaged (of kShort for 16 rows at d = 128), either
+// layout, for batches whose groups share a prefix.
 enum Build { kShort = 0, kLong = 1, kPaged = 2, kShared = 3 };
 
 // The instantiations for head dimension DH and K width BK (defined in
@@ -1144,7 +1144,12 @@ template <int BK, int BV, bool QJL, int NT, int DH, bool SHARED>
 DecodeVariant variant_c(int build) {
   constexpr int smem = decode_smem_bytes<BK, BV, QJL, NT, DH>();
   if constexpr (SHARED) {
-    return {decode_mma_kernel<BK, BV, QJL, NT, DH == 256 ? 2 : 3, true, DH, true>, smem};
+    // 16 rows at d = 128 keep their accumulators in the 168-register budget; at
+    // 128 they spill (300 bytes a thread, 560 with QJL), and three CTAs per SM were
+    // slower than two: 3/3 bits, 16 rows behind 65536 positions 60 us against 57,
+    // 16 groups behind 4096 72 against 69; 2/4 bits with QJL 106 against 100
+    constexpr int C = DH == 256 || (DH == 128 && NT == 2) ? 2 : 3;
+    return {decode_mma_kernel<BK, BV, QJL, NT, C, true, DH, true>, smem};
   } else if constexpr (DH == 128) {
     if (build == kPaged) return {decode_mma_kernel<BK, BV, QJL, NT, 3, true, DH>, smem};
     if (build == kLong) return {decode_mma_kernel<BK, BV, QJL, NT, 3, false, DH>, smem};

@@ -25,8 +25,8 @@ namespace {
 
 // Rows of a group above which the tcgen05 prefix pass runs.  One group, 8 KV
 // heads, 3/3 bits, the whole call, tcgen05 / 16-row tiles: 16 rows, 8192 shared
-// positions 27 / 29 us, 65536 73 / 62; 20 rows 25 / 32 and 73 / 88; 64 rows 31 / 44
-// and 75 / 160; 128 rows 39 / 65 and 86 / 305.
+// positions 25 / 27 us, 65536 71 / 56; 20 rows 25 / 28 and 72 / 83; 64 rows 31 / 42
+// and 75 / 145; 128 rows 38 / 58 and 84 / 277.
 constexpr int kTcMinRows = 16;
 constexpr int kTcFixed = 4;      // a tcgen05 CTA's prologue and partial, in tile times (8 us; a tile takes 2)
 constexpr int kSuffixFixed = 1;  // a CTA's prologue in the 16-row passes, in stages of 128 positions
@@ -150,9 +150,9 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
     // the count with the fewest stage times over all waves, counted in halves of
     // a stage, and a tenth of one for each split (its CTA's prologue beside
     // others, and the merge).  Whole calls, 3/3 bits, 8 KV heads, 16 rows: 8192
-    // shared positions, 18 splits 30 us, 24 28, 43 32, 64 40; 65536, 36 splits 75,
-    // 55 60, 74 (two waves) 76; 16 groups of 4096, 2 splits 85, 3 72, 4 86.  With
-    // QJL the prologue has a second product (128 rows, 16384: 4 splits 188, 8 201).
+    // shared positions, 18 splits 28 us, 22 26, 26 27, 37 26; 65536, 27 splits 63,
+    // 37 57, 46 (two waves) 74; 16 groups of 4096, 1 split 95, 2 69, 3 80.  With
+    // QJL the prologue has a second product (128 rows, 16384: 4 splits 164, 8 181).
     const long fixed = qjl ? 3 : kSuffixFixed;
     const long halves = (max_prefix + 63) / 64, lanes = (long)s.units * n_kv_heads;
     const long slots = (long)sm_count() * shared_ctas_per_sm(d, bits_k, bits_v, qjl, s.nt_p);
