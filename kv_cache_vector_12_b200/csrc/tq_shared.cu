@@ -42,26 +42,27 @@ struct MergeArgs {
   float *lse;
 };
 
-// kMergeRows (sequence, query head) rows per CTA of 128 threads: a warp joins
-// the split partials of one row, then every thread takes output coordinate
-// `tid` (and tid + 128 at d = 256) of all of them, so that a row of Pi^T is
-// loaded once for kMergeRows rows.  One row per CTA, as the merge of
+// kMergeRows (sequence, query head) rows per CTA: a warp joins the split partials
+// of one row, then every thread takes output coordinate `tid` of all of them, so
+// that a row of Pi^T is loaded once for kMergeRows rows.  One row per CTA, as the merge of
 // tq_decode_attention has it, reads Pi^T (32 KB) for every row: 21 us for 1024
-// rows of 25 partials, where this takes 11.5 for 1024 rows of 19.
+// rows of 25 partials, where this takes 11.5 for 1024 rows of 19.  At d = 256 a row
+// of Pi^T (512 bytes) is too long for a thread: 8 warps take 32 coordinates each,
+// a coordinate's row over the lanes (16 rows 43 us with two rows read by a thread).
 constexpr int kMergeRows = 4;
+constexpr int merge_threads(int dh) { return dh == 256 ? 256 : 128; }
 
 template <int DH>
-__global__ void __launch_bounds__(128) shared_merge_kernel(const MergeArgs a, int n_rows) {
+__global__ void __launch_bounds__(merge_threads(DH)) shared_merge_kernel(const MergeArgs a, int n_rows) {
   constexpr int PF = DH + 4, PL = DH / 32;
   __shared__ __align__(16) float s_ot[kMergeRows][DH];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row0 = blockIdx.x * kMergeRows, row = row0 + warp;
-  Bf16Row<DH> pw0, pw1;
-  if (tid < DH) pw0.load(a.p.pivt + tid * DH);
-  if constexpr (DH == 256) pw1.load(a.p.pivt + (tid + 128) * DH);
+  Bf16Row<DH> pw;  // (DH = 256: unused)
+  if (DH < 256 && tid < DH) pw.load(a.p.pivt + tid * DH);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (row < n_rows) {
+  if (warp < kMergeRows && row < n_rows) {
     const int s = row / a.n_q_heads;
     const SeqRange g = sequence_range(a.cu_group, a.prefix, a.n_groups, a.seq_lens, a.max_group, a.max_prefix,
                                       a.max_suffix, a.capacity, s, lane);
@@ -110,11 +111,48 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const MergeArgs a, in
     if (a.out_f32) static_cast<float *>(a.out)[at] = x;
     else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(x);
   };
+  if constexpr (DH < 256) {
 #pragma unroll
-  for (int e = 0; e < kMergeRows; ++e) {
-    if (row0 + e >= n_rows) break;
-    if (tid < DH) store(e, tid, dot_bf16_row<DH>(pw0, s_ot[e]));
-    if constexpr (DH == 256) store(e, tid + 128, dot_bf16_row<DH>(pw1, s_ot[e]));
+    for (int e = 0; e < kMergeRows; ++e) {
+      if (row0 + e >= n_rows) break;
+      if (tid < DH) store(e, tid, dot_bf16_row<DH>(pw, s_ot[e]));
+    }
+  } else {
+    static_assert(kMergeRows == 4, "the sums below are those of four rows");
+    float x[kMergeRows][8];  // entries 8 lane .. 8 lane + 7 of every row
+#pragma unroll
+    for (int e = 0; e < kMergeRows; ++e) load_floats<8>(s_ot[e] + 8 * lane, x[e]);
+    __syncthreads();  // (s_ot takes the outputs)
+#pragma unroll 8
+    for (int o = 0; o < 32; ++o) {
+      const int i = 32 * warp + o;
+      const uint4 v = reinterpret_cast<const uint4 *>(a.p.pivt + (size_t)i * DH)[lane];
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      float sum[kMergeRows];
+#pragma unroll
+      for (int e = 0; e < kMergeRows; ++e) {
+        sum[e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          sum[e] = fmaf(__uint_as_float(u[c] << 16), x[e][2 * c], sum[e]);
+          sum[e] = fmaf(__uint_as_float(u[c] & 0xffff0000u), x[e][2 * c + 1], sum[e]);
+        }
+      }
+      // sums over the lanes, row lane / 8 in every lane: halves change rows first
+      const bool b4 = lane & 16, b3 = lane & 8;
+      float s0 = b4 ? sum[2] : sum[0], s1 = b4 ? sum[3] : sum[1];
+      s0 += __shfl_xor_sync(0xffffffffu, b4 ? sum[0] : sum[2], 16);
+      s1 += __shfl_xor_sync(0xffffffffu, b4 ? sum[1] : sum[3], 16);
+      float t = b3 ? s1 : s0;
+      t += __shfl_xor_sync(0xffffffffu, b3 ? s0 : s1, 8);
+#pragma unroll
+      for (int m = 4; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+      if ((lane & 7) == 0) s_ot[lane >> 3][i] = t;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kMergeRows; ++e)
+      if (row0 + e < n_rows) store(e, tid, s_ot[e][tid]);
   }
 }
 
@@ -257,7 +295,7 @@ int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q
                     args.partials, out, out_f32, lse};
   const int n_rows = c.n_seqs * n_q_heads;
   cfg.gridDim = dim3((unsigned)((n_rows + kMergeRows - 1) / kMergeRows));
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(merge_threads(p.d));
   cfg.dynamicSmemBytes = 0;
   const auto merge = p.d == 64 ? shared_merge_kernel<64> : p.d == 256 ? shared_merge_kernel<256> : shared_merge_kernel<128>;
   return (int)cudaLaunchKernelEx(&cfg, merge, m, n_rows);
