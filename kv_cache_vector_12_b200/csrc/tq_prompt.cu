@@ -133,7 +133,8 @@ __device__ __forceinline__ float f(uint32_t x) { return __uint_as_float(x); }
 // (added and subtracted 1.5 2^23), a polynomial of degree 5 for 2^f on
 // [-1/2, 1/2] (minimax of the relative error, fitted by weighted least squares:
 // 2.3e-7 in fp32, what ex2.approx has), and n added to the exponent.  Below
-// 2^-126 the result is some number under 2^-125 rather than 0.
+// 2^-126 the result is some number under 2^-125 rather than 0.  NaN and +inf are
+// lost here: the row's maximum finds them.
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
   x.x = fmaxf(x.x, -126.f);
   x.y = fmaxf(x.y, -126.f);
@@ -465,6 +466,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
       const int t = row / G, pos = (row < PC * G && base + t < len) ? base + t : -1;
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
       const uint32_t t_o = tmem + C::o_col(i) + lanes;
+      const float kNan = __int_as_float(0x7fc00000);
       float ref = 0.f, l = 0.f;
       bool ok = true;
       if constexpr (C::kQTmem) {
@@ -513,11 +515,14 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) mx = max3(mx, f(v[c][e]), f(v[c][e + 1]));
+          for (int e = 0; e < 32; e += 2) mx = max3_nan(mx, f(v[c][e]), f(v[c][e + 1]));
         mx *= a.c;
+        // A row with a score of NaN or +inf is NaN (inf - inf): its sum becomes NaN
+        // here, as the maximum tells, since exp2_fma keeps neither.
         if (h == 0) {
           ref = fmaxf(mx, kFloor);
-        } else if (__any_sync(0xffffffffu, pos >= 0 && mx > ref + kLazy)) {  // (rows of no query hold anything)
+          if (!(mx < INFINITY)) l = kNan;
+        } else if (__any_sync(0xffffffffu, pos >= 0 && !(mx <= ref + kLazy))) {  // (rows of no query hold anything)
           // O is rescaled once the values of step h - 1 are in it: the scores of
           // step h + 1 were issued behind them (in front of the last step nothing
           // was, so those have a barrier of their own)
@@ -527,7 +532,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
           tc_fence_after();
           const float nref = fmaxf(ref, mx), al = ex2(ref - nref);
           ref = nref;
-          l *= al;
+          l = mx < INFINITY ? l * al : kNan;
 #pragma unroll 1
           for (int c = 0; c < DH / 32; ++c) {
             uint32_t o[32];
@@ -592,7 +597,7 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
           // floor) has no weights but what the polynomial puts for 2^-inf:
           // o = 0 / 0 and lse = -inf, or NaN where a score was one
           if (!(ref > kFloor)) l *= 0.f;
-          const float il = l > 0.f ? 1.f / l : __int_as_float(0x7fc00000);
+          const float il = l > 0.f ? 1.f / l : kNan;
           const long orow = pos < 0 ? 0 : (long)(tok0 + pos) * a.n_q_heads + h_kv * G + row % G;
 #pragma unroll 1
           for (int c = 0; c < DH / 32; ++c) {

@@ -325,3 +325,24 @@ def test_two_calls_at_once(tq):
     torch.cuda.synchronize()
     ctx.check_device_errors()
     assert all(torch.equal(o, ref) for o in outs)
+
+
+@pytest.mark.parametrize("kind", ["nan", "inf"])
+@pytest.mark.parametrize("d,max_len", [(64, 330), (64, 2200), (128, 330), (128, 2200), (256, 330)])
+def test_one_key_of_nan_or_infinity_reaches_every_later_query(tq, d, max_len, kind):
+    """A score of NaN or +inf makes its row NaN, wherever in a key tile the key lies and however many steps later the
+    query; the rows before it stay within their bounds.  (The bound on the lengths selects the form.)"""
+    ctx, n = context(tq, d), 330
+    q, k, v = rows(2200, 2, d, 1), rows(2200, 1, d, 2), rows(2200, 1, d, 3)
+    q[:, :, 0] = q[:, :, 0].abs() + 1      # (+inf in a key's first coordinate is then a score of +inf)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    for j in range(64, 128):
+        kk = k.clone()
+        kk[j] = float("nan") if kind == "nan" else kk[j]
+        kk[j, :, 0] = float(kind)
+        out, lse = torch.zeros(2200, 2, d, device="cuda"), torch.zeros(2200, 2, device="cuda")
+        tq.prompt_attention(ctx, q, kk, v, cu, max_len, out, lse)
+        assert out[j:n].isnan().all() and not torch.isfinite(lse[j:n]).any(), j
+        # (the rows before the key see none of it: the formula over those alone)
+        check(q, kk, v, out, lse, [j], [0])
+    ctx.check_device_errors()
