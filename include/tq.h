@@ -361,8 +361,9 @@ size_t tq_shared_workspace_bytes(const tq_ctx *ctx, const tq_cache *cache,
  * the block that holds the prefix's end on, and only if it has positions
  * there; entries before it may hold anything.  The first sequence's table has
  * to hold the prefix only if some member takes part.  A sequence outside every
- * group, in a group of more than max_group, or with lengths outside the bounds
- * gets out = 0, lse = -inf and sets the seq_len flag of tq_check_device_errors.
+ * group, in a group of more than max_group or one that ends behind n_seqs, or
+ * with lengths outside the bounds gets out = 0, lse = -inf and sets the seq_len
+ * flag of tq_check_device_errors; where cu_group decreases, every sequence does.
  * out, lse and the workspace may not overlap an input or one another.  The
  * workspace holds nothing between calls: calls one behind the other may use the
  * same one, calls (and replayed graphs) that may run at the same time each need

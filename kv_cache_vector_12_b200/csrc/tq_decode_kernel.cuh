@@ -334,7 +334,7 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
       t_end = len;
     } else {
       const SeqRange g = sequence_range(a.cu_group, a.prefix, a.n_groups, a.seq_lens, a.max_group, a.max_prefix,
-                                        a.max_suffix, a.c.capacity, s, lane);
+                                        a.max_suffix, a.c.capacity, a.c.n_seqs, s, lane);
       if (g.bad && tid == 0 && split == 0 && h == 0) atomicOr(a.p.err, kErrSeqLen);
       if (g.len <= g.prefix) return;
       t_low = g.prefix;

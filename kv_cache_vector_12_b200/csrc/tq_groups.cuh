@@ -62,7 +62,9 @@ __device__ __forceinline__ bool any_member(const int32_t *seq_lens, const Shared
 
 // What sequence s attends over: its group's prefix [0, prefix) and its own
 // [prefix, len).  Length 0: no part.  bad: outside every group, or its group or
-// lengths outside the call's bounds; its len and prefix are then 0.
+// lengths outside the call's bounds, or cu decreasing somewhere (groups would
+// overlap); its len and prefix are then 0.  Every group that is not bad here is
+// one that find_members cuts into units.
 struct SeqRange {
   int group, prefix, len;
   bool bad;
@@ -70,17 +72,22 @@ struct SeqRange {
 
 __device__ __forceinline__ SeqRange sequence_range(const int32_t *cu, const int32_t *prefix, int n_groups,
                                                    const int32_t *seq_lens, int max_group, int max_prefix,
-                                                   int max_suffix, int capacity, int s, int lane) {
+                                                   int max_suffix, int capacity, int n_seqs, int s, int lane) {
   SeqRange r = {0, 0, 0, true};
   const int len = seq_lens[s];
   // the last group that begins at or before s: groups are counted by the warp
   int count = 0;
-  for (int g = lane; g < n_groups; g += 32) count += cu[g] <= s;
+  bool ordered = true;
+  for (int g = lane; g < n_groups; g += 32) {
+    const int b = cu[g];
+    count += b <= s;
+    ordered &= b <= cu[g + 1];
+  }
   count = (int)__reduce_add_sync(0xffffffffu, (unsigned)count);
-  if (count == 0) return r;
+  if (!__all_sync(0xffffffffu, ordered) || count == 0) return r;
   const int g = count - 1;
-  const int p = prefix[g];
-  if (s >= cu[g + 1] || cu[g] < 0 || cu[g + 1] - cu[g] > max_group) return r;
+  const int p = prefix[g], b = cu[g], e = cu[g + 1];
+  if (s >= e || b < 0 || e > n_seqs || e - b > max_group) return r;
   if (len == 0) {
     r.group = g;
     r.bad = false;

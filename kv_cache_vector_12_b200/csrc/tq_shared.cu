@@ -34,7 +34,7 @@ constexpr int kSuffixFixed = 1;  // a CTA's prologue in the 16-row passes, in st
 struct MergeArgs {
   DeviceParams p;
   const int32_t *seq_lens, *cu_group, *prefix;
-  int n_groups, max_group, max_prefix, max_suffix, capacity, n_q_heads;
+  int n_groups, max_group, max_prefix, max_suffix, capacity, n_seqs, n_q_heads;
   int p_chunk, p_splits, s_chunk, s_splits;
   const float *partials;
   void *out;
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(merge_threads(DH)) shared_merge_kernel(const M
   if (warp < kMergeRows && row < n_rows) {
     const int s = row / a.n_q_heads;
     const SeqRange g = sequence_range(a.cu_group, a.prefix, a.n_groups, a.seq_lens, a.max_group, a.max_prefix,
-                                      a.max_suffix, a.capacity, s, lane);
+                                      a.max_suffix, a.capacity, a.n_seqs, s, lane);
     // the slots in use: the splits that hold positions, of either pass
     const int n_p = g.len > 0 && a.p_splits ? (g.prefix + a.p_chunk - 1) / a.p_chunk : 0;
     const int n_s = g.len > g.prefix ? (g.len - (g.prefix & ~63) + a.s_chunk - 1) / a.s_chunk : 0;
@@ -290,9 +290,9 @@ int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q
     const cudaError_t e = cudaLaunchKernelEx(&cfg, v.fn, args);
     if (e != cudaSuccess) return (int)e;
   }
-  const MergeArgs m{p,          seq_lens,   cu_group,  prefix,       n_groups,      max_group,    max_prefix,
-                    max_suffix, c.capacity, n_q_heads, plan.p_chunk, plan.p_splits, plan.s_chunk, plan.s_splits,
-                    args.partials, out, out_f32, lse};
+  const MergeArgs m{p,          seq_lens,   cu_group, prefix,    n_groups,     max_group,     max_prefix,
+                    max_suffix, c.capacity, c.n_seqs, n_q_heads, plan.p_chunk, plan.p_splits, plan.s_chunk,
+                    plan.s_splits, args.partials, out, out_f32, lse};
   const int n_rows = c.n_seqs * n_q_heads;
   cfg.gridDim = dim3((unsigned)((n_rows + kMergeRows - 1) / kMergeRows));
   cfg.blockDim = dim3(merge_threads(p.d));

@@ -445,3 +445,23 @@ def test_two_calls_at_once(tq, n, per):
     torch.cuda.synchronize()
     b.ctx.check_device_errors()
     assert all(torch.equal(o, ref) for o in outs)
+
+
+@pytest.mark.parametrize("per", [4, 8])
+def test_groups_that_end_behind_the_batch_or_decrease_are_flagged(tq, per):
+    """Groups that the prefix pass cannot cut into units (16 rows per CTA with 4 query heads per KV head, tcgen05 with
+    8): their sequences are 0, whatever the workspace held, and the others right."""
+    def flagged(b, skip, **kw):
+        out, lse = b.call(**kw)
+        with pytest.raises(tq.TQError) as ei:
+            b.ctx.check_device_errors()
+        assert ei.value.status == tq.TQ_ERR_DEVICE and "seq_len" in str(ei.value)
+        for s in skip:
+            assert (out[s] == 0).all() and (lse[s] == -math.inf).all(), s
+        b.check(out, lse, skip=skip)
+
+    flagged(Batch(tq, [0, 2, 6], [100, 200], [150, 110, 220, 201], per=per), [2, 3])
+    flagged(Batch(tq, [0, 2, 2 ** 31 - 1], [100, 200], [150, 110, 220, 201], per=per), [2, 3], max_group=4)
+    lens = [300 + s for s in range(8)]
+    for groups in ([4, 6, 0, 8], [0, 5, 3, 8], [0, 8, 0, 8]):
+        flagged(Batch(tq, groups, [300, 290, 280], lens, per=per), range(8), max_group=8)
