@@ -456,9 +456,10 @@ tq_status tq_prompt_attention(tq_ctx *ctx, const void *q, const void *k,
  * a sequence with a negative length or more than capacity tokens gets none
  * and seq_lens = 0 (bit 1); a prefix that is negative, no multiple of
  * block_size, longer than the member's cached_lens or than the first member's
- * tokens is not shared (bit 1); when the free list runs out, or an entry lies
- * outside [0, n_blocks), the table entry and the slots become -1, free_end at
- * most n_free (bit 0); rows past n_tok are not written (bit 0).
+ * tokens is not shared (bit 1), and none is where cu_group decreases (bit 1);
+ * when the free list runs out, or an entry lies outside [0, n_blocks), the table
+ * entry and the slots become -1, free_end at most n_free (bit 0); rows past
+ * n_tok are not written (bit 0).
  * The same call on the same inputs writes the same outputs, so a captured
  * call may be replayed.  Asynchronous on `stream`, one kernel, allocates
  * nothing.  Errors: TQ_ERR_INVALID, TQ_ERR_UNSUPPORTED (n_seqs), TQ_ERR_CUDA.

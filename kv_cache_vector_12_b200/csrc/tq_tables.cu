@@ -115,15 +115,19 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
     s_blk[s] = paged ? blocks_of(a, c + w) - blocks_of(a, c) : 0;
     if (blockIdx.x == 0) a.seq_lens[s] = c + w;
   }
+  bool ordered = true;  // (groups that overlap would copy entries that others are writing)
   for (int g = tid; g <= a.n_groups; g += kTabThreads)
-    if (a.n_groups) s_g[g] = a.cu_group[g];
+    if (a.n_groups) {
+      s_g[g] = a.cu_group[g];
+      ordered &= g == a.n_groups || s_g[g] <= a.cu_group[g + 1];
+    }
   int start = 0;
   if (paged) {
     start = *a.free_start;
     if (start < 0 || start > a.n_free) start = a.n_free;
   }
-  if (bad && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
-  __syncthreads();
+  if ((bad || !ordered) && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
+  const bool groups = __syncthreads_and(ordered) && a.n_groups > 0;
 
   // ---- the two exclusive sums, side by side: half of the threads takes the
   // tokens, half the blocks, every thread a run of consecutive sequences
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
   // ---- shared prefixes: every member but the first takes the first one's
   // entries, a warp per sequence.  An entry that the first member gets in this
   // call is taken from the free list again, so nothing waits for its store.
-  if (a.n_groups == 0) return;
+  if (!groups) return;
   for (int s = blockIdx.x * kTabWarps + warp; s < a.n_seqs; s += gridDim.x * kTabWarps) {
     if (s < s_g[0]) continue;
     const int g = last_at_most(s_g, a.n_groups, s);

@@ -281,3 +281,20 @@ def test_the_most_tokens(tq, ctx):
             assert torch.equal(b["pos"][i:j], torch.arange(i - a, j - a, dtype=torch.int32, device="cuda"))
     for x in (b["seq_idx"], b["pos"]):
         assert x.as_strided((1,), (1,), n).item() == -7
+
+
+@pytest.mark.parametrize("groups", [[0, 5, 3, 8], [4, 6, 0, 8], [0, 8, 0, 8]])
+def test_groups_that_decrease_share_nothing(tq, ctx, groups):
+    """Groups that overlap would copy table entries that others write: flagged, the rest of the step as without them."""
+    ids = np.arange(40, dtype=np.int32)
+    cached, new = [128] * 8, [1] * 8
+    table, used = start_table(cached, 64, 256, ids)
+    ref = reference(cached, new, table, 64, 256, ids[used:], 0)
+    cache = tq.PagedCache(ctx, 8, 1, 256, 64, n_blocks=40, block_table=torch.from_numpy(table))
+    b = buffers(8, 8)
+    tq.build_tables(ctx, cache, dev(cached), dev(new), **b, free_list=dev(ids[used:]), free_start=dev([0]),
+                    cu_group=dev(groups), prefix_lens=dev([128, 128, 128]))
+    assert "seq_len" in _flagged(tq, ctx)
+    assert np.array_equal(cache.block_table.cpu().numpy(), ref["table"])
+    for k in ("seq_idx", "pos", "slots", "cu_new", "seq_lens"):
+        assert b[k].tolist() == ref[k], k
