@@ -326,9 +326,13 @@ tq_status tq_decode_attention_noalloc(tq_ctx *ctx, const tq_cache *cache,
                                       int32_t max_seq_len, float scale,
                                       float *out, float *lse, void *stream);
 
-/* Device workspace (bytes) that tq_decode_attention_shared needs for these
- * sizes; 0 for sizes that the call refuses.  Of `cache` n_seqs, n_kv_heads and
- * the layout are used; the context's device must be current. */
+/* Device workspace (bytes) with which tq_decode_attention_shared runs its
+ * fastest split for these sizes; 0 for sizes that the call refuses.  Of `cache`
+ * n_seqs, n_kv_heads and the layout are used; the context's device must be
+ * current.  The split follows waves of thread blocks, so a smaller call may have
+ * the larger number; with less the call splits less.  What it needs at least is
+ * n_seqs * n_q_heads * (d + 4) * 4 bytes, twice that with max_prefix_len > 0, so
+ * a workspace made for the largest sizes serves every call of smaller ones. */
 size_t tq_shared_workspace_bytes(const tq_ctx *ctx, const tq_cache *cache,
                                  int32_t n_q_heads, int32_t n_groups,
                                  int32_t max_group, int32_t max_prefix_len,
@@ -364,7 +368,9 @@ size_t tq_shared_workspace_bytes(const tq_ctx *ctx, const tq_cache *cache,
  * group, in a group of more than max_group or one that ends behind n_seqs, or
  * with lengths outside the bounds gets out = 0, lse = -inf and sets the seq_len
  * flag of tq_check_device_errors; where cu_group decreases, every sequence does.
- * out, lse and the workspace may not overlap an input or one another.  The
+ * out, lse and the workspace may not overlap an input or one another.
+ * workspace_bytes chooses the split together with the bounds (see
+ * tq_shared_workspace_bytes): other sizes may change the last bits.  The
  * workspace holds nothing between calls: calls one behind the other may use the
  * same one, calls (and replayed graphs) that may run at the same time each need
  * their own.  A capacity of more than 2^30 is TQ_ERR_UNSUPPORTED.

@@ -616,9 +616,9 @@ tq_status check_shared_sizes(const tq_cache *cache, int32_t n_q_heads, int32_t n
 }
 
 tq::SharedPlan shared_plan(const tq_ctx *ctx, const tq_cache *cache, int32_t n_q_heads, int32_t n_groups,
-                           int32_t max_group, int32_t max_prefix_len, int32_t max_suffix_len) {
+                           int32_t max_group, int32_t max_prefix_len, int32_t max_suffix_len, size_t room) {
   return tq::plan_shared(ctx->d, ctx->bits_k, ctx->bits_v, ctx->qjl, cache->n_seqs, n_q_heads, cache->n_kv_heads,
-                         n_groups, max_group, max_prefix_len, max_suffix_len);
+                         n_groups, max_group, max_prefix_len, max_suffix_len, room);
 }
 
 }  // namespace
@@ -628,7 +628,9 @@ size_t tq_shared_workspace_bytes(const tq_ctx *ctx, const tq_cache *cache, int32
   if (!ctx || check_geometry(cache) != TQ_OK || tq::check_context_device(ctx) != TQ_OK ||
       check_shared_sizes(cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len) != TQ_OK)
     return 0;
-  return shared_plan(ctx, cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len).workspace;
+  const size_t bytes =
+      shared_plan(ctx, cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len, SIZE_MAX).workspace;
+  return (bytes + 255) / 256 * 256;
 }
 
 tq_status tq_decode_attention_shared(tq_ctx *ctx, const tq_cache *cache, const void *q, int32_t q_dtype,
@@ -660,7 +662,7 @@ tq_status tq_decode_attention_shared(tq_ctx *ctx, const tq_cache *cache, const v
              {prefix_lens, 4 * (size_t)n_groups}}))
     return fail(TQ_ERR_INVALID, "out, lse or the workspace overlaps another argument");
   const tq::SharedPlan plan =
-      shared_plan(ctx, cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len);
+      shared_plan(ctx, cache, n_q_heads, n_groups, max_group, max_prefix_len, max_suffix_len, workspace_bytes);
   if (workspace_bytes < plan.workspace)
     return fail(TQ_ERR_INVALID, "workspace_bytes=%zu < required %zu", workspace_bytes, plan.workspace);
   if (scale <= 0.f) scale = 1.0f / std::sqrt((float)ctx->d);

@@ -181,8 +181,10 @@ struct SharedPlan {
   int s_chunk, s_splits;     // its split of [prefix rounded down to 64, len)
   size_t workspace;          // partials [n_seqs n_q_heads][p_splits + s_splits][d + 4]
 };
+// The fastest plan that fits `room` bytes; where none does (less than one slot
+// a row for either pass), the smallest, whose `workspace` is what is needed.
 SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n_q_heads, int n_kv_heads, int n_groups,
-                       int max_group, int max_prefix, int max_suffix);
+                       int max_group, int max_prefix, int max_suffix, size_t room);
 int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q_dtype, int n_q_heads,
                   const int32_t *seq_lens, const int32_t *cu_group, const int32_t *prefix, int n_groups,
                   int max_group, int max_prefix, int max_suffix, float scale, void *out, bool out_f32, float *lse,

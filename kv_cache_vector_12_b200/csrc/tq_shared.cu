@@ -29,6 +29,7 @@ namespace {
 // and 75 / 145; 128 rows 38 / 58 and 84 / 277.
 constexpr int kTcMinRows = 16;
 constexpr int kTcFixed = 4;      // a tcgen05 CTA's prologue and partial, in tile times (8 us; a tile takes 2)
+constexpr int kMaxPrefixSplits = 128, kMaxSuffixSplits = 64;
 constexpr int kSuffixFixed = 1;  // a CTA's prologue in the 16-row passes, in stages of 128 positions
 
 struct MergeArgs {
@@ -158,8 +159,11 @@ __global__ void __launch_bounds__(merge_threads(DH)) shared_merge_kernel(const M
 
 }  // namespace
 
-SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n_q_heads, int n_kv_heads, int n_groups,
-                       int max_group, int max_prefix, int max_suffix) {
+namespace {
+
+// plan_shared with at most p_most and s_most splits.
+SharedPlan plan_splits(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n_q_heads, int n_kv_heads, int n_groups,
+                       int max_group, int max_prefix, int max_suffix, long p_most, long s_most) {
   SharedPlan s = {};
   const int per = n_q_heads / n_kv_heads;
   s.tc = d == kHeadDim && !qjl && (long)per * max_group > kTcMinRows;
@@ -175,7 +179,7 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
     // (q rotation) and its partial
     const long tiles = (max_prefix + 127) / 128, lanes = (long)s.units * n_kv_heads, sms = sm_count();
     long best = -1;
-    for (long n = 1; n <= tiles && n <= 128; ++n) {
+    for (long n = 1; n <= tiles && n <= p_most; ++n) {
       const long per_split = (tiles + n - 1) / n, used = (tiles + per_split - 1) / per_split;
       const long cost = (lanes * used + sms - 1) / sms * (per_split + kTcFixed);
       if (best < 0 || cost < best) {
@@ -195,7 +199,7 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
     const long halves = (max_prefix + 63) / 64, lanes = (long)s.units * n_kv_heads;
     const long slots = (long)sm_count() * shared_ctas_per_sm(d, bits_k, bits_v, qjl, s.nt_p);
     long best = -1;
-    for (long n = 1; n <= halves && n <= 128; ++n) {
+    for (long n = 1; n <= halves && n <= p_most; ++n) {
       const long per_split = (halves + n - 1) / n, used = (halves + per_split - 1) / per_split;
       const long cost = 5 * ((lanes * used + slots - 1) / slots * (per_split + 2 * fixed)) + used;
       if (best < 0 || cost < best) {
@@ -215,7 +219,7 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
     const long stages = (max_suffix + 63 + 127) / 128, units = (long)n_seqs * n_kv_heads;
     const long slots = (long)sm_count() * shared_ctas_per_sm(d, bits_k, bits_v, qjl, s.nt_s);
     long best = -1;
-    for (long n = 1; n <= stages && n <= 64; ++n) {
+    for (long n = 1; n <= stages && n <= s_most; ++n) {
       const long per_split = (stages + n - 1) / n, used = (stages + per_split - 1) / per_split;
       const long cost = (units * used + slots - 1) / slots * (per_split + kSuffixFixed);
       if (best < 0 || cost < best) {
@@ -226,8 +230,27 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
     }
   }
   const size_t rows = (size_t)n_seqs * n_q_heads;
-  s.workspace = (rows * (size_t)(s.p_splits + s.s_splits) * (size_t)(d + 4) * sizeof(float) + 255) / 256 * 256;
+  s.workspace = rows * (size_t)(s.p_splits + s.s_splits) * (size_t)(d + 4) * sizeof(float);
   return s;
+}
+
+}  // namespace
+
+SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n_q_heads, int n_kv_heads, int n_groups,
+                       int max_group, int max_prefix, int max_suffix, size_t room) {
+  const auto plan = [&](long p_most, long s_most) {
+    return plan_splits(d, bits_k, bits_v, qjl, n_seqs, n_q_heads, n_kv_heads, n_groups, max_group, max_prefix, max_suffix,
+                       p_most, s_most);
+  };
+  const SharedPlan s = plan(kMaxPrefixSplits, kMaxSuffixSplits);
+  if (s.workspace <= room) return s;
+  // Fewer slots than the fastest counts take (they follow waves, and a smaller
+  // call may want more than a larger one): both passes in proportion, one at least.
+  const long slots = (long)(room / ((size_t)n_seqs * n_q_heads * (size_t)(d + 4) * sizeof(float)));
+  if (s.p_splits == 0) return plan(0, slots > 1 ? slots : 1);
+  const long total = s.p_splits + s.s_splits, p = (slots * s.p_splits + total / 2) / total;
+  const long p_most = p < 1 ? 1 : p > slots - 1 && slots > 1 ? slots - 1 : p;
+  return plan(p_most, slots - p_most > 1 ? slots - p_most : 1);
 }
 
 int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q_dtype, int n_q_heads,

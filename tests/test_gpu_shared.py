@@ -465,3 +465,53 @@ def test_groups_that_end_behind_the_batch_or_decrease_are_flagged(tq, per):
     lens = [300 + s for s in range(8)]
     for groups in ([4, 6, 0, 8], [0, 5, 3, 8], [0, 8, 0, 8]):
         flagged(Batch(tq, groups, [300, 290, 280], lens, per=per), range(8), max_group=8)
+
+
+@pytest.mark.parametrize("d,qjl,n_kv,per,sizes,prefix", [(128, 0, 8, 4, [32], 2560), (128, 0, 2, 4, [4] * 8, 3584),
+                                                        (128, 1, 2, 7, [8] * 2, 3584), (64, 0, 2, 4, [5, 3], 3840),
+                                                        (256, 0, 2, 2, [2, 9], 3840)])
+def test_a_workspace_for_the_largest_bounds_serves_smaller_ones(tq, d, qjl, n_kv, per, sizes, prefix):
+    """The fastest split of a smaller call may take more slots: it then runs with those there are."""
+    groups, n = [0] + np.cumsum(sizes).tolist(), sum(sizes)
+    n_q, ms = n_kv * per, 200
+    b = Batch(tq, groups, [prefix] * len(sizes), [prefix + 1 + s % 60 for s in range(n)], n_kv=n_kv, d=d, qjl=qjl, per=per,
+              seed=d)
+    size = tq.shared_workspace_bytes(b.ctx, b.cache, n_q, len(sizes), max(sizes), prefix, ms)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for p in (prefix, prefix - 64, prefix - 128, prefix - 192, prefix - 256, prefix // 2, 100, 1):
+        for suffix in (60, ms):
+            b.prefixes = [p] * len(sizes)
+            b.lens = [p + 1 + s % 60 for s in range(n)]
+            for norms in ("norm_k", "norm_v", "qjl_norm"):  # (no NaN outside the first call's positions: p is below)
+                if norms in b.planes:
+                    x = b.planes[norms]
+                    b.planes[norms] = np.where(x == -1, np.float16(1).view(np.int16), x)
+                    b.cache.planes[norms].copy_(torch.from_numpy(b.planes[norms]))
+            ws.fill_(0xFF)
+            out, lse = b.call(workspace=ws, max_suffix=suffix)
+            b.ctx.check_device_errors()
+            b.check(out, lse, skip=[s for s in range(n) if s % 7], heads_of=(1,))
+    # pairs behind the same prefix, each held by its own first sequence
+    b.groups = list(range(0, n, 2)) + [n]
+    b.prefixes = [100] * (len(b.groups) - 1)
+    b.group_of = [s // 2 for s in range(n)]
+    b.lens = [101 + s % 60 for s in range(n)]
+    out, lse = b.call(workspace=ws, max_suffix=ms)
+    b.ctx.check_device_errors()
+    b.check(out, lse, heads_of=(1,))
+
+
+def test_the_smallest_workspace(tq):
+    """One slot a row for the prefixes and one behind them; without prefixes one; a byte less is refused."""
+    for n, d, qjl in ((3, 128, 0), (30, 128, 0), (3, 128, 1), (3, 64, 0), (5, 256, 0)):
+        for prefix in (1500, 0):
+            b = Batch(tq, [0, n], [prefix], [prefix + 300 + s for s in range(n)], d=d, qjl=qjl)
+            least = n * 8 * (d + 4) * 4 * (2 if prefix else 1)
+            ws = torch.full((least + 1024,), 0xFF, dtype=torch.uint8, device="cuda")
+            out, lse = b.call(workspace=ws[:least])
+            b.ctx.check_device_errors()
+            b.check(out, lse, skip=range(5, n))
+            assert (ws[least:] == 0xFF).all()
+            with pytest.raises(tq.TQError) as ei:
+                b.call(workspace=ws[:least - 1])
+            assert ei.value.status == tq.TQ_ERR_INVALID and "workspace" in str(ei.value)
