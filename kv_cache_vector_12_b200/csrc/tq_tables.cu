@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
   }
 
   // ---- per-token maps: a row per thread, or (VEC) four, in one 16-byte store
-  // per map (two for the slots) where they lie in one block of one sequence
+  // per map (two for the slots) where they lie in one sequence, and paged in one
+  // block of it
   constexpr int kTokVec = VEC ? 4 : 1;
   const int rows = min(total_tok, a.n_tok);
   const unsigned stride = gridDim.x * kTabThreads;  // (unsigned: an index past 2^31 - 1 ends its loop)
@@ -180,7 +181,8 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
     const int r0 = (int)at;
     int s = last_at_most(s_tok, a.n_seqs, r0);
     const int c = s_c[s], p = c + (r0 - s_tok[s]);
-    if (VEC && min(rows, s_tok[s + 1]) - r0 >= kTokVec && block_of(a, p) == block_of(a, p + kTokVec - 1)) {
+    if (VEC && min(rows, s_tok[s + 1]) - r0 >= kTokVec &&
+        (!paged || block_of(a, p) == block_of(a, p + kTokVec - 1))) {
       *reinterpret_cast<int4 *>(a.seq_idx + r0) = make_int4(s, s, s, s);
       *reinterpret_cast<int4 *>(a.pos + r0) = make_int4(p, p + 1, p + 2, p + 3);
       if (a.slots) {

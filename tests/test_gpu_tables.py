@@ -298,3 +298,27 @@ def test_groups_that_decrease_share_nothing(tq, ctx, groups):
     assert np.array_equal(cache.block_table.cpu().numpy(), ref["table"])
     for k in ("seq_idx", "pos", "slots", "cu_new", "seq_lens"):
         assert b[k].tolist() == ref[k], k
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+def test_contiguous_cache_with_more_tokens_than_resident_threads(tq, ctx, offset):
+    """Four rows to a thread in the contiguous layout: sequences that begin and end inside its four, of odd lengths."""
+    rng = np.random.default_rng(offset)
+    cached, new, capacity = rng.integers(0, 500, 90), rng.integers(0, 9000, 90), 9600
+    new[3:9] = [1, 0, 2, 3, 0, 1]
+    n_tok = int(new.sum())
+    cache = tq.Cache(ctx, 90, 1, 64)
+    cache.struct.capacity = capacity  # (no plane is used)
+    b = buffers(90, n_tok + offset + 5)
+    del b["free_end"]
+    view = {k: b[k][offset:] if k in ("seq_idx", "pos", "slots") else b[k] for k in b}
+    tq.build_tables(ctx, cache, dev(cached), dev(new), **view)
+    ctx.check_device_errors()
+    seq = np.repeat(np.arange(90), new)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    pos = np.arange(n_tok) - cu[seq] + cached[seq]
+    for k, ref in (("seq_idx", seq), ("pos", pos), ("slots", seq * capacity + pos)):
+        got = b[k].cpu().numpy()
+        assert np.array_equal(got[offset:offset + n_tok], ref), k
+        assert (got[:offset] == FILL).all() and (got[offset + n_tok:] == FILL).all(), k
+    assert np.array_equal(b["cu_new"].cpu().numpy(), cu) and np.array_equal(b["seq_lens"].cpu().numpy(), cached + new)
