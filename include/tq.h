@@ -481,6 +481,16 @@ tq_status tq_build_tables(tq_ctx *ctx, const tq_cache *cache,
                           void *stream);
 
 /*
+ * The three calls above with their arguments in one array of 64-bit words, in
+ * order: pointers and integers (sign-extended; a word that does not fit its
+ * argument is TQ_ERR_INVALID), scale as a double.  For bindings whose calls cost
+ * by the argument.
+ */
+tq_status tq_decode_attention_shared_words(const void *words); /* 19 words */
+tq_status tq_prompt_attention_words(const void *words);        /* 18 words */
+tq_status tq_build_tables_words(const void *words);            /* 19 words */
+
+/*
  * Synchronise `stream`, then report and clear the context's sticky
  * device-side error flags: TQ_OK, or TQ_ERR_DEVICE with a message naming the
  * flags (bit 0: a token outside the cache in tq_quantize, or a paged

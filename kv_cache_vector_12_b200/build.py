@@ -27,7 +27,7 @@ SOURCES = [(s, os.path.splitext(s)[0], []) for s in
            ["tq_host.cpp", "tq_fragments.cpp", "tq_api.cu", "tq_kernels.cu", "tq_quantize_tc.cu",
             "tq_quantize_qjl_tc.cu", "tq_quantize_tc256.cu", "tq_decode.cu", "tq_prefill.cu", "tq_weight.cu",
             "tq_noalloc.cu", "tq_tables.cu", "tq_prompt.cu", "tq_shared.cu",
-            "tq_shared_tc.cu"]]
+            "tq_shared_tc.cu", "tq_words.cpp"]]
 SOURCES += [(f"{name}.cu", f"{name}_d{d}_k{bk}", [f"-DTQ_DECODE_DH={d}", f"-DTQ_DECODE_BK={bk}"])
             for name in ("tq_decode_variants", "tq_shared_variants") for d in (64, 128, 256) for bk in (2, 3, 4)]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

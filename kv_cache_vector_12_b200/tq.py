@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -22,6 +23,7 @@ TQ_OK, TQ_ERR_INVALID, TQ_ERR_CUDA, TQ_ERR_NOMEM, TQ_ERR_UNSUPPORTED, TQ_ERR_DEV
 TQ_BF16, TQ_F32 = 0, 1
 TQ_LAW_GAUSSIAN, TQ_LAW_SPHERE = 0, 1
 LAWS = {"gaussian": TQ_LAW_GAUSSIAN, "sphere": TQ_LAW_SPHERE}
+_MAX_TABLE_SEQS = 4096  # of tq_build_tables
 PLANES = ("codes_k", "norm_k", "qjl_bits", "qjl_norm", "codes_v", "norm_v")
 
 _vp = ctypes.c_void_p
@@ -80,6 +82,13 @@ lib.tq_prompt_attention.restype = ctypes.c_int
 lib.tq_build_tables.argtypes = [_vp, ctypes.POINTER(tq_cache), _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32,
                                 _i32, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.tq_build_tables.restype = ctypes.c_int
+# The arguments of a call as one array of words (a ctypes call costs 0.1 us for each argument)
+_SHARED_WORDS = struct.Struct("QQQqqQQQqqqqdQqQQQQ").pack
+_PROMPT_WORDS = struct.Struct("QQQQqqqqqqQqqdQqQQ").pack
+_TABLES_WORDS = struct.Struct("QQQQQQqQQQQqqQQQQQQ").pack
+for _call in (lib.tq_decode_attention_shared_words, lib.tq_prompt_attention_words, lib.tq_build_tables_words):
+    _call.argtypes = [ctypes.c_char_p]
+    _call.restype = ctypes.c_int
 lib.tq_check_device_errors.argtypes = [_vp, _vp]
 lib.tq_check_device_errors.restype = ctypes.c_int
 lib.tq_last_error.argtypes = []
@@ -109,6 +118,39 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_device = torch._C._cuda_getDevice  # torch.cuda.current_device() without its check that CUDA is set up
+_current_stream = torch._C._cuda_getCurrentRawStream
+_address = ctypes.addressof
+_F32, _BF16, _I32, _I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+_INT, _OUT_TYPES = (_I32,), (_BF16, _F32)
+
+
+def _handle(ctx) -> int:
+    return ctx.handle.value if ctx.handle else 0
+
+
+def _ints(arrays, dev: int) -> list | None:
+    """The addresses of contiguous int32 tensors on device `dev`; None if one is not that."""
+    at = []
+    for t in arrays:
+        if t is None or t.dtype is not _I32 or not t.is_contiguous() or t.get_device() != dev:
+            return None
+        at.append(t.data_ptr())
+    return at
+
+
+def _refuse(call: str, dev: int, *arrays) -> None:
+    """The error for the first of (name, tensor or None, element types, least number of elements) that does not fit:
+    the library gets a bare pointer, so a tensor of another type, layout, device or size is refused before the call.
+    (None is left to the library.)  A call tests its arrays itself, in one expression, and comes here when one fails."""
+    for name, t, dtypes, n in arrays:
+        if t is None or (t.dtype in dtypes and t.numel() >= n and t.is_contiguous() and t.get_device() == dev):
+            continue
+        raise TQError(TQ_ERR_INVALID, f"{call}: {name} must be a contiguous tensor of {dtypes} on the current CUDA device "
+                                      f"with at least {n} elements, not {t.dtype} {tuple(t.shape)}, strides {t.stride()}, "
+                                      f"on {t.device}")
 
 
 def _fbuf(t: torch.Tensor | None):
@@ -296,13 +338,27 @@ def decode_attention_shared(ctx: Context, cache: Cache, q: torch.Tensor, seq_len
     (cu_group int32 [n_groups + 1]) that share their first prefix_lens[g]
     (int32 [n_groups]) positions, read from the group's first sequence; q
     [n_seqs, n_q_heads, d] bf16 or fp32, out bf16 or fp32 of the same shape."""
-    q_dtype = TQ_F32 if q.dtype == torch.float32 else TQ_BF16
-    out_dtype = TQ_F32 if out.dtype == torch.float32 else TQ_BF16
-    _check(lib.tq_decode_attention_shared(ctx.handle, ctypes.byref(cache.struct), _ptr(q), q_dtype, q.shape[1],
-                                          _ptr(seq_lens), _ptr(cu_group), _ptr(prefix_lens), prefix_lens.numel(),
-                                          max_group, max_prefix_len, max_suffix_len, scale, _ptr(out), out_dtype,
-                                          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                          _stream(stream)))
+    _, n_q, d = q.shape
+    n_seqs, n_groups = cache.struct.n_seqs, prefix_lens.numel()
+    rows, dev = n_seqs * n_q, _device()
+    if not (_ints((seq_lens, cu_group, prefix_lens), dev) and d == ctx.d and seq_lens.numel() >= n_seqs
+            and cu_group.numel() > n_groups and q.dtype in _OUT_TYPES and q.numel() >= rows * d and q.is_contiguous()
+            and out.dtype in _OUT_TYPES and out.numel() >= rows * d and out.is_contiguous() and workspace.is_contiguous()
+            and q.get_device() == out.get_device() == workspace.get_device() == dev
+            and (lse is None or lse.dtype is _F32 and lse.numel() >= rows and lse.is_contiguous()
+                 and lse.get_device() == dev)):
+        if n_q <= 16 * cache.struct.n_kv_heads:  # (more are refused by the library as unsupported)
+            _refuse("decode_attention_shared", dev, ("q", q, _OUT_TYPES, rows * d), ("seq_lens", seq_lens, _INT, n_seqs),
+                    ("cu_group", cu_group, _INT, n_groups + 1), ("prefix_lens", prefix_lens, _INT, 0),
+                    ("out", out, _OUT_TYPES, rows * d), ("lse", lse, (_F32,), rows),
+                    ("workspace", workspace, (workspace.dtype,), 0))
+            if d != ctx.d:
+                raise TQError(TQ_ERR_INVALID, f"decode_attention_shared: q of head dimension {d}, not {ctx.d}")
+    _check(lib.tq_decode_attention_shared_words(_SHARED_WORDS(
+        _handle(ctx), _address(cache.struct), q.data_ptr(), TQ_F32 if q.dtype is _F32 else TQ_BF16, n_q,
+        _ptr(seq_lens) or 0, _ptr(cu_group) or 0, prefix_lens.data_ptr(), n_groups, max_group, max_prefix_len,
+        max_suffix_len, scale, out.data_ptr(), TQ_F32 if out.dtype is _F32 else TQ_BF16, _ptr(lse) or 0,
+        workspace.data_ptr(), workspace.nbytes, _current_stream(dev) if stream is None else _stream(stream))))
 
 
 def prompt_attention(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -313,16 +369,30 @@ def prompt_attention(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Te
     n_q_heads, d], k and v bf16 [n_tok, n_kv_heads, d] (slices of one fused
     projection are taken by their token stride); out bf16 or fp32 [n_tok,
     n_q_heads, d], lse fp32 [n_tok, n_q_heads]."""
-    n_tok, n_q_heads, d = q.shape
+    (n_tok, n_q, d), (k_tok, n_kv, k_d), (v_tok, v_heads, v_d) = q.shape, k.shape, v.shape
     (q0, q1, q2), (k0, k1, k2), (v0, v1, v2) = q.stride(), k.stride(), v.stride()
-    if not (q.dtype is k.dtype is v.dtype is torch.bfloat16 and q1 == k1 == v1 == d == ctx.d and q2 == k2 == v2 == 1
+    if not (q.dtype is k.dtype is v.dtype is _BF16 and q1 == k1 == v1 == d == ctx.d and q2 == k2 == v2 == 1
             and out.is_contiguous()):
         raise TQError(TQ_ERR_INVALID, "prompt_attention takes bf16 q, k, v with the heads of a token contiguous, "
                                       "and a contiguous out")
-    out_dtype = TQ_F32 if out.dtype is torch.float32 else TQ_BF16
-    _check(lib.tq_prompt_attention(ctx.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, k0, v0, n_tok, n_q_heads,
-                                   k.shape[1], _ptr(cu_seqlens), cu_seqlens.numel() - 1, max_len, scale,
-                                   out.data_ptr(), out_dtype, _ptr(lse), _stream(stream)))
+    dev = _device()
+    if not (k_tok >= n_tok <= v_tok and n_kv == v_heads and k_d == v_d == d
+            and q.get_device() == k.get_device() == v.get_device() == dev):
+        raise TQError(TQ_ERR_INVALID, f"prompt_attention: k {tuple(k.shape)} on {k.device} and v {tuple(v.shape)} on "
+                                      f"{v.device} must have the same heads and d, at least the tokens of q {tuple(q.shape)} "
+                                      f"on {q.device}, and all be on the current CUDA device")
+    rows = n_tok * n_q
+    if not (cu_seqlens.dtype is _I32 and cu_seqlens.is_contiguous() and out.dtype in _OUT_TYPES
+            and out.numel() >= rows * d and cu_seqlens.get_device() == out.get_device() == dev
+            and (lse is None or lse.dtype is _F32 and lse.numel() >= rows and lse.is_contiguous()
+                 and lse.get_device() == dev)):
+        if n_q <= 16 * n_kv:  # (more are refused by the library as unsupported)
+            _refuse("prompt_attention", dev, ("cu_seqlens", cu_seqlens, _INT, 0), ("out", out, _OUT_TYPES, rows * d),
+                    ("lse", lse, (_F32,), rows))
+    _check(lib.tq_prompt_attention_words(_PROMPT_WORDS(
+        _handle(ctx), q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, k0, v0, n_tok, n_q, n_kv, cu_seqlens.data_ptr(),
+        cu_seqlens.numel() - 1, max_len, scale, out.data_ptr(), TQ_F32 if out.dtype is _F32 else TQ_BF16,
+        _ptr(lse) or 0, _current_stream(dev) if stream is None else _stream(stream))))
 
 
 def build_tables(ctx: Context, cache: Cache, cached_lens: torch.Tensor, new_lens: torch.Tensor, seq_idx: torch.Tensor,
@@ -337,14 +407,38 @@ def build_tables(ctx: Context, cache: Cache, cached_lens: torch.Tensor, new_lens
     free_start (int32 [1]); free_end (int32 [1]) is where the next step
     starts.  cu_group (int32 [n_groups + 1]) and prefix_lens (int32
     [n_groups]): groups of sequences that begin with the same blocks."""
-    table = getattr(cache, "block_table", None)
-    p = [None if t is None else t.data_ptr()
-         for t in (table, cached_lens, new_lens, free_list, free_start, free_end, cu_group, prefix_lens, seq_idx, pos,
-                   slots, cu_new, seq_lens)]
-    _check(lib.tq_build_tables(ctx.handle, ctypes.byref(cache.struct), p[0], p[1], p[2], p[3],
-                               0 if free_list is None else free_list.numel(), p[4], p[5], p[6], p[7],
-                               0 if prefix_lens is None else prefix_lens.numel(), seq_idx.numel(), p[8], p[9], p[10],
-                               p[11], p[12], _stream(stream)))
+    table, n_seqs, n_tok, dev = getattr(cache, "block_table", None), cache.struct.n_seqs, seq_idx.numel(), _device()
+    ints, n_free, n_groups = [cached_lens, new_lens, seq_idx, pos, cu_new, seq_lens], 0, 0
+    if prefix_lens is not None:
+        n_groups = prefix_lens.numel()
+        ints += cu_group, prefix_lens
+    if table is not None:
+        n_free = 0 if free_list is None else free_list.numel()
+        ints += free_list, free_start, free_end
+        if table.data_ptr() != cache.struct.block_table:
+            raise TQError(TQ_ERR_INVALID, "build_tables: cache.block_table is not the table that the cache was made with")
+    p = _ints(ints, dev)
+    if not (p and cached_lens.numel() >= n_seqs <= new_lens.numel() and pos.numel() >= n_tok
+            and cu_new.numel() > n_seqs <= seq_lens.numel() and (not n_groups or cu_group.numel() > n_groups)
+            and (table is None or free_start.numel() and free_end.numel())
+            and (slots is None or slots.dtype is _I64 and slots.numel() >= n_tok and slots.is_contiguous()
+                 and slots.get_device() == dev)):
+        if n_seqs <= _MAX_TABLE_SEQS:  # (more are refused by the library as unsupported)
+            _refuse("build_tables", dev, ("cached_lens", cached_lens, _INT, n_seqs), ("new_lens", new_lens, _INT, n_seqs),
+                    ("seq_idx", seq_idx, _INT, 0), ("pos", pos, _INT, n_tok), ("slots", slots, (_I64,), n_tok),
+                    ("cu_new", cu_new, _INT, n_seqs + 1), ("seq_lens", seq_lens, _INT, n_seqs),
+                    ("cu_group", cu_group if n_groups else None, _INT, n_groups + 1),
+                    ("prefix_lens", prefix_lens, _INT, 0))
+            if table is not None:
+                _refuse("build_tables", dev, ("free_list", free_list, _INT, 0), ("free_start", free_start, _INT, 1),
+                        ("free_end", free_end, _INT, 1))
+        p = [0 if t is None else t.data_ptr() for t in ints]
+    groups = p[6:8] if prefix_lens is not None else (0, 0)
+    free = p[-3:] if table is not None else (0, 0, 0)
+    _check(lib.tq_build_tables_words(_TABLES_WORDS(
+        _handle(ctx), _address(cache.struct), 0 if table is None else table.data_ptr(), p[0], p[1], free[0], n_free,
+        free[1], free[2], *groups, n_groups, n_tok, p[2], p[3], 0 if slots is None else slots.data_ptr(), p[4], p[5],
+        _current_stream(dev) if stream is None else _stream(stream))))
 
 
 class WeightCache:

@@ -138,3 +138,35 @@ def test_admit_join_and_decode(tq, bits_k, bits_v, qjl, tails):
             ok, w = ph.attention_ok(dout[s, hh].cpu().numpy(), o_ref, dlse[s, hh].cpu().numpy(), l_ref,
                                     np.abs(scores).max(axis=1))
             assert ok, (s, h, w)
+
+
+def test_host_tensors_and_other_types_are_refused(tq):
+    """Tensors that the kernels could not read are refused before the launch, and nothing is written."""
+    ctx = tq.Context(D, 3, 3, 0, 42)
+    cache = tq.PagedCache(ctx, 2, H, CAP, BS)
+
+    def refused(call, good, **changed):
+        for name, t in changed.items():
+            with pytest.raises(tq.TQError) as ei:
+                call(**{**good, name: t})
+            assert ei.value.status == tq.TQ_ERR_INVALID, name
+        ctx.check_device_errors()
+
+    new = lambda n: torch.full((n,), -7, dtype=torch.int32, device="cuda")  # noqa: E731
+    step = dict(cached_lens=_ints(0, 0), new_lens=_ints(1, 1), seq_idx=new(2), pos=new(2), cu_new=new(3), seq_lens=new(2),
+                free_list=_ints(4, 5), free_start=_ints(0), free_end=new(1))
+    refused(lambda **kw: tq.build_tables(ctx, cache, **kw), step, cached_lens=torch.zeros(2, dtype=torch.int32),
+            new_lens=_ints(1, 1).long(), pos=new(1), cu_new=new(2), seq_lens=new(4)[::2], free_end=new(0))
+    assert all((step[k] == -7).all() for k in ("seq_idx", "pos", "cu_new", "seq_lens", "free_end"))
+    q = torch.randn(30, H * PER, D, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    prompt = dict(q=q, k=q[:, :H], v=q[:, :H], cu_seqlens=_ints(0, 30), max_len=30, out=out)
+    refused(lambda **kw: tq.prompt_attention(ctx, **kw), prompt, k=q[:29, :H], v=q[:, :1], out=out[:29],
+            cu_seqlens=_ints(0, 30).cpu(), lse=torch.empty(30, H * PER, dtype=torch.float64, device="cuda"))
+    refused(lambda **kw: tq.prompt_attention(ctx, **kw), prompt, out=out.half())
+    ws = tq.alloc_shared_workspace(ctx, cache, H * PER, 1, 2, 64, 64)
+    shared = dict(q=q[:2], seq_lens=_ints(70, 80), cu_group=_ints(0, 2), prefix_lens=_ints(64), max_group=2,
+                  max_prefix_len=64, max_suffix_len=64, out=out[:2], lse=None, workspace=ws)
+    refused(lambda **kw: tq.decode_attention_shared(ctx, cache, **kw), shared, q=q[:1], seq_lens=_ints(70, 80).long(),
+            cu_group=_ints(0), out=out[:2].half(), workspace=ws.cpu(), prefix_lens=_ints(64).cpu())
+    assert (out == 7.0).all()
