@@ -67,8 +67,10 @@ struct DecodeArgs {
   int members;                       // sequences per CTA of the prefix pass
   int slot0;                         // first partial slot of this pass (n_splits counts both passes' slots)
   // the pass behind the prefixes runs beside the prefix pass, launched before
-  // it: only CTA (0, 0, n_seqs), which has no other work, waits for that grid
+  // it: only CTA (0, 0, n_seqs), which has no other work, waits for that grid;
+  // the others take over what it waited for with `token` (tq_groups.cuh)
   bool beside;
+  unsigned long long token;
 };
 
 enum SharedPass { kPassPrefix = 0, kPassSuffix = 1 };
@@ -301,20 +303,26 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (SHARED && a.beside && tid == 32 * kConsumerWarps && (int)blockIdx.z < a.c.n_seqs) {
+    take_over(token_word(a.partials), a.token);
+    // (this thread issues the bulk copies)
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+  }
   __syncthreads();
   // launched as a programmatic dependent: the cache, q and seq_lens are final
   // once the previous kernel in the stream has completed
   if constexpr (SHARED) {
     // Every CTA of the prefix pass lets the next grid start as soon as the
-    // kernels in front of the call have completed, so that grid may read
-    // whatever they wrote without waiting; the merge behind it waits for it,
-    // and so through its last CTA for the prefix pass.
+    // kernels in front of the call have completed; that grid took over what they
+    // wrote (above) instead of waiting.  The merge behind it waits for it, and so
+    // through its last CTA for the prefix pass.
     const bool last = a.beside && (int)blockIdx.z == a.c.n_seqs;
     if (last ? blockIdx.x + blockIdx.y == 0 : !a.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (last) return;
-    // (no line of theirs that this SM may still hold from an earlier kernel is read)
-    if (a.beside) __threadfence();
-    if (a.pass == kPassPrefix) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (a.pass == kPassPrefix && tid == 0) {
+      if (blockIdx.x + blockIdx.y + blockIdx.z == 0) hand_on(token_word(a.partials), a.token);
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }

@@ -60,6 +60,31 @@ __device__ __forceinline__ bool any_member(const int32_t *seq_lens, const Shared
   return __any_sync(0xffffffffu, any);
 }
 
+// The pass behind the prefixes runs beside the prefix pass, before that grid has
+// completed, and reads what the kernels in front of the call wrote.  Those are
+// visible to the prefix pass, which waited for them; its first thread hands them
+// on by a store-release of the call's token, and every CTA of the other pass
+// acquires it: causality order takes the writes along.  (The prefix grid lets the
+// next one start after that store, so the token is there at the first look;
+// should it not be, the wait for the whole prefix grid serves as well.)  The
+// merge clears the word, so that a replayed call does not meet its own token.
+__device__ __forceinline__ void hand_on(unsigned long long *word, unsigned long long token) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(word), "l"(token) : "memory");
+}
+__device__ __forceinline__ void take_over(const unsigned long long *word, unsigned long long token) {
+  for (int i = 0; i < 64; ++i) {
+    unsigned long long x;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(word) : "memory");
+    if (x == token) return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// That word: the two floats of the first partial that hold nothing (a partial is
+// m, l, two unused, the outputs).
+__device__ __forceinline__ unsigned long long *token_word(float *partials) {
+  return reinterpret_cast<unsigned long long *>(partials + 2);
+}
+
 // What sequence s attends over: its group's prefix [0, prefix) and its own
 // [prefix, len).  Length 0: no part.  bad: outside every group, or its group or
 // lengths outside the call's bounds, or cu decreasing somewhere (groups would

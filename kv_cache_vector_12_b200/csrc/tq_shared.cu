@@ -14,6 +14,8 @@
 // The passes are the decode attention kernel in its SHARED build
 // (tq_decode_kernel.cuh), up to 16 rows per CTA; groups of more rows at d = 128
 // without QJL take the prefix pass of tq_shared_tc.cu, up to 128 rows per CTA.
+#include <atomic>
+#include <chrono>
 #include <cmath>
 
 #include "tq_decode_kernel.cuh"
@@ -37,7 +39,7 @@ struct MergeArgs {
   const int32_t *seq_lens, *cu_group, *prefix;
   int n_groups, max_group, max_prefix, max_suffix, capacity, n_seqs, n_q_heads;
   int p_chunk, p_splits, s_chunk, s_splits;
-  const float *partials;
+  float *partials;
   void *out;
   bool out_f32;
   float *lse;
@@ -63,6 +65,7 @@ __global__ void __launch_bounds__(merge_threads(DH)) shared_merge_kernel(const M
   if (DH < 256 && tid < DH) pw.load(a.p.pivt + tid * DH);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0 && tid == 0 && a.p_splits) *token_word(a.partials) = 0;
   if (warp < kMergeRows && row < n_rows) {
     const int s = row / a.n_q_heads;
     const SeqRange g = sequence_range(a.cu_group, a.prefix, a.n_groups, a.seq_lens, a.max_group, a.max_prefix,
@@ -253,6 +256,23 @@ SharedPlan plan_shared(int d, int bits_k, int bits_v, int qjl, int n_seqs, int n
   return plan(p_most, slots - p_most > 1 ? slots - p_most : 1);
 }
 
+namespace {
+
+// A number that no earlier call of the process had and that a workspace does not
+// hold by chance: a counter from a start of its own, mixed (SplitMix64's step).
+unsigned long long next_token() {
+  static std::atomic<uint64_t> count{0};
+  static const uint64_t start =
+      (uint64_t)std::chrono::system_clock::now().time_since_epoch().count() ^ ((uint64_t)(uintptr_t)&count << 20);
+  uint64_t z = start + 0x9E3779B97F4A7C15ull * (count.fetch_add(1, std::memory_order_relaxed) + 1);
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  z ^= z >> 31;
+  return z ? z : 1;
+}
+
+}  // namespace
+
 int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q_dtype, int n_q_heads,
                   const int32_t *seq_lens, const int32_t *cu_group, const int32_t *prefix, int n_groups,
                   int max_group, int max_prefix, int max_suffix, float scale, void *out, bool out_f32, float *lse,
@@ -282,10 +302,12 @@ int launch_shared(const DeviceParams &p, const tq_cache &c, const void *q, int q
   args.max_prefix = max_prefix;
   args.max_suffix = max_suffix;
   args.members = plan.members;
+  args.token = next_token();
   cfg.blockDim = dim3(kThreads);
   if (plan.p_splits > 0 && plan.tc) {
     const SharedTcArgs t{p,      c,        n_q_heads, q,          q_dtype,      scale,        seq_lens,      cu_group,
-                         prefix, n_groups, max_group, max_prefix, plan.members, plan.p_chunk, args.partials, args.n_splits};
+                         prefix, n_groups, max_group, max_prefix, plan.members, plan.p_chunk, args.partials, args.n_splits,
+                         args.token};
     cfg.gridDim = dim3(plan.p_splits, c.n_kv_heads, plan.units);
     const int e = launch_shared_prefix_tc(t, cfg);
     if (e != 0) return e;

@@ -122,9 +122,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_prefix_tc_kernel(const S
         *reinterpret_cast<const uint4 *>(a.p.pi + (size_t)a.p.kperm[row] * D + c);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (the pass behind the prefix may start: it reads what the kernels in front
-  // of the call wrote, and the merge waits for both)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (the pass behind the prefix may start: it takes over what the kernels in
+  // front of the call wrote, and the merge waits for both)
+  if (tid == 0) {
+    if (blockIdx.x + blockIdx.y + blockIdx.z == 0) hand_on(token_word(a.partials), a.token);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   const SharedUnit u = find_members(a.cu_group, a.n_groups, a.max_group, a.members, a.c.n_seqs, blockIdx.z, lane);
   if (u.count == 0) return;
   const int prefix = a.prefix[u.group];

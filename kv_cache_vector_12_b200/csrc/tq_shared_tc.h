@@ -20,6 +20,7 @@ struct SharedTcArgs {
   int chunk;         // positions per split, a multiple of 128
   float *partials;   // [rows][n_slots][d + 4], this pass's splits first
   int n_slots;
+  unsigned long long token;  // of the call, for the pass beside this one (tq_groups.cuh)
 };
 
 // Launches on cfg's stream and grid; returns a cudaError_t as int.

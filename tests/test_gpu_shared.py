@@ -515,3 +515,53 @@ def test_the_smallest_workspace(tq):
             with pytest.raises(tq.TQError) as ei:
                 b.call(workspace=ws[:least - 1])
             assert ei.value.status == tq.TQ_ERR_INVALID and "workspace" in str(ei.value)
+
+
+@pytest.mark.parametrize("n,per,qjl", [(4, 4, 0), (40, 4, 0), (6, 7, 1)])
+def test_inputs_written_just_before_the_call(tq, n, per, qjl):
+    """The pass behind the prefixes does not wait for the prefix pass, and still reads what the kernels in front of the
+    call wrote: queries, lengths and cached bytes that change right before every call, captured and replayed, and a
+    workspace that was used, is new or is filled in between."""
+    b = Batch(tq, [0, n], [700], [900 + s % 60 for s in range(n)], per=per, qjl=qjl)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    groups, prefixes, lens = ints(b.groups), ints(b.prefixes), ints(b.lens)
+    ws = tq.alloc_shared_workspace(b.ctx, b.cache, b.n_kv * per, 1, n, 700, 260)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    planes = [t for t in b.cache.planes.values() if t is not None and t.dtype == torch.uint8]
+    sets = [([torch.randint(0, 256, t.shape, generator=g, device="cuda", dtype=torch.uint8) for t in planes],
+             torch.randn(b.q.shape, generator=g, device="cuda"), lens - 13 * i) for i in range(4)]
+    src = [[t.clone() for t in sets[0][0]], sets[0][1].clone(), sets[0][2].clone()]
+    out, lse = torch.zeros_like(b.q), torch.zeros(b.q.shape[:2], device="cuda")
+
+    def step():
+        for t, x in zip(planes, src[0]):
+            t.copy_(x)
+        b.q.copy_(src[1])
+        lens.copy_(src[2])
+        tq.decode_attention_shared(b.ctx, b.cache, b.q, lens, groups, prefixes, n, 700, 260, out, lse, ws)
+
+    def select(i):
+        for t, x in zip([*src[0], src[1], src[2]], [*sets[i][0], sets[i][1], sets[i][2]]):
+            t.copy_(x)
+
+    refs = []
+    for i in range(4):
+        select(i)
+        torch.cuda.synchronize()
+        step()
+        torch.cuda.synchronize()
+        refs.append((out.clone(), lse.clone()))
+    assert not any(torch.equal(refs[0][0], r[0]) for r in refs[1:])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    got = []
+    for i in range(60):
+        select(i % 4)
+        if i % 3 == 0:
+            ws.fill_(i)
+        graph.replay() if i % 2 else step()
+        got.append((out.clone(), lse.clone()))
+    b.ctx.check_device_errors()
+    for i, (x, y) in enumerate(got):
+        assert torch.equal(x, refs[i % 4][0]) and torch.equal(y, refs[i % 4][1]), i
