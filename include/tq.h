@@ -344,7 +344,8 @@ size_t tq_shared_workspace_bytes(const tq_ctx *ctx, const tq_cache *cache,
  * cu_group[g + 1] - 1 form group g, positions [0, prefix_lens[g]) of all of
  * them are read from the group's first sequence, once for the whole group,
  * and positions [prefix_lens[g], seq_lens[s]) from sequence s itself.  Scores,
- * softmax and values are those of tq_decode_attention over the union.
+ * softmax and values are those of tq_decode_attention over the union; a query
+ * row with a NaN or an infinity gets NaN (there it is not told apart).
  *  cu_group     device int32 [n_groups + 1], cu_group[0] = 0, non-decreasing,
  *               cu_group[n_groups] = n_seqs (a group may be empty or hold one
  *               sequence).

@@ -519,17 +519,23 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
           if (f32) mma_bf16(c[nt], alo[0], alo[1], alo[2], alo[3], b0, b1);
         }
       }
-      // per head: mu = 32767 / max |q_hat|, q_hat as 16-bit fixed point (hi, lo bytes)
+      // per head: mu = 32767 / max |q_hat|, q_hat as 16-bit fixed point (hi, lo bytes).
+      // SHARED: the maximum keeps NaN, and makes the row's score factor NaN (an
+      // integer cannot be), as in the tcgen05 prefix pass.
+      const auto top = [](float x, float y, float z) {
+        if constexpr (SHARED) return max3_nan(x, y, z);
+        else return fmaxf(x, fmaxf(y, z));
+      };
       float mx0 = 0.f, mx1 = 0.f;  // rows r, r + 8
 #pragma unroll
       for (int nt = 0; nt < NTW; ++nt) {
-        mx0 = fmaxf(mx0, fmaxf(fabsf(c[nt][0]), fabsf(c[nt][1])));
-        mx1 = fmaxf(mx1, fmaxf(fabsf(c[nt][2]), fabsf(c[nt][3])));
+        mx0 = top(mx0, fabsf(c[nt][0]), fabsf(c[nt][1]));
+        mx1 = top(mx1, fabsf(c[nt][2]), fabsf(c[nt][3]));
       }
 #pragma unroll
       for (int o = 1; o <= 2; o <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        mx0 = top(mx0, mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+        mx1 = top(mx1, mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
       }
       if (q == 0) {
         s_red[warp][r] = mx0;
@@ -541,7 +547,7 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
       for (int e = 0; e < 2; ++e) {
         if (kRows <= 8 && e == 1) break;
         const int row = r + 8 * e;
-        const float m = fmaxf(fmaxf(s_red[0][row], s_red[1][row]), fmaxf(s_red[2][row], s_red[3][row]));
+        const float m = top(top(s_red[0][row], s_red[0][row], s_red[1][row]), s_red[2][row], s_red[3][row]);
         mu[e] = m > 0.f ? 32767.f / m : 1.f;
         qmax[e] = m;
       }
@@ -561,6 +567,10 @@ __global__ void __maxnreg__(CTAS == 3 ? 128 : 168) decode_mma_kernel(const Decod
       if (warp == 0 && q == 0) {
         s_qs[r][0] = a.scale * kLog2e / (mu[0] * ldexpf(1.f, a.p.k_shift));
         if constexpr (kRows > 8) s_qs[r + 8][0] = a.scale * kLog2e / (mu[1] * ldexpf(1.f, a.p.k_shift));
+        if constexpr (SHARED) {
+          if (isnan(qmax[0])) s_qs[r][0] = qmax[0];
+          if (kRows > 8 && isnan(qmax[1])) s_qs[r + 8][0] = qmax[1];
+        }
       }
       if constexpr (QJL) {
         // q_tilde = S' q_hat (rows of S in the QJL fragment order, columns in

@@ -565,3 +565,23 @@ def test_inputs_written_just_before_the_call(tq, n, per, qjl):
     b.ctx.check_device_errors()
     for i, (x, y) in enumerate(got):
         assert torch.equal(x, refs[i % 4][0]) and torch.equal(y, refs[i % 4][1]), i
+
+
+@pytest.mark.parametrize("d,qjl,n", [(64, 0, 3), (128, 0, 3), (128, 1, 3), (256, 0, 3), (128, 0, 40)])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_a_query_of_nan_or_infinity_makes_its_row_nan(tq, d, qjl, n, value, prefix):
+    """One coordinate of one head's query: that row is NaN in both passes, every other row right."""
+    b = Batch(tq, [0, n], [prefix], [prefix + 40 + s for s in range(n)], d=d, qjl=qjl)
+    clean, clean_lse = b.call()
+    b.check(clean, clean_lse, skip=range(5, n))
+    b.q[1, 2, 5] = float(value)
+    out, lse = b.call()
+    b.ctx.check_device_errors()
+    assert out[1, 2].isnan().all() and lse[1, 2].isnan()
+    others = torch.ones_like(lse, dtype=torch.bool)
+    others[1, 2] = False
+    # (the same inputs, and a row's maximum moves with no other row's: the same bits but for tcgen05 rescales of a
+    # warp's rows together, whose factor of 1 is exact and whose moved references round anew)
+    err = (out - clean).abs().amax(-1) / clean.abs().amax(-1)
+    assert (err[others] <= 1e-3).all()
