@@ -452,7 +452,8 @@ tq_status tq_prompt_attention(tq_ctx *ctx, const void *q, const void *k,
  * the same prefix_lens[g] tokens (device int32 [n_groups], multiples of
  * block_size), and the first prefix_lens[g] / block_size entries of every
  * member but the first become the first member's.  Such a member counts the
- * prefix in its cached_lens.  n_groups = 0: none (cu_group and prefix_lens
+ * prefix in its cached_lens; one without tokens (cached and new both 0, a place
+ * of a padded batch) keeps its entries.  n_groups = 0: none (cu_group and prefix_lens
  * may be NULL); a contiguous cache has no table and ignores the groups.
  * Of `cache` only n_seqs (at most 4096), capacity, block_table, block_size
  * and n_blocks are used (n_kv_heads and the planes are not).  For a contiguous

@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
     const int g = last_at_most(s_g, a.n_groups, s);
     const int lead = s_g[g];
     if (s >= s_g[g + 1] || s == lead) continue;
+    if (s_c[s] == 0 && s_tok[s + 1] == s_tok[s]) continue;  // no tokens: takes no part (a padded batch)
     const int prefix = a.prefix[g];
     // (lengths out of bounds count as 0 here, and were flagged above)
     const int cl = lead >= 0 ? s_c[lead] : 0;

@@ -322,3 +322,21 @@ def test_contiguous_cache_with_more_tokens_than_resident_threads(tq, ctx, offset
         assert np.array_equal(got[offset:offset + n_tok], ref), k
         assert (got[:offset] == FILL).all() and (got[offset + n_tok:] == FILL).all(), k
     assert np.array_equal(b["cu_new"].cpu().numpy(), cu) and np.array_equal(b["seq_lens"].cpu().numpy(), cached + new)
+
+
+def test_members_without_tokens_keep_their_entries(tq, ctx):
+    """A padded batch: finished members of a group, and a group of nothing else, are no error and change nothing."""
+    ids = np.random.default_rng(3).permutation(40).astype(np.int32)
+    cached, new, prefix = [192, 0, 192, 0, 0, 0, 128], [1, 0, 70, 0, 0, 0, 1], 128
+    groups = [0, 4, 6, 7]
+    table, used = start_table(cached, 64, 320, ids)
+    ref = reference(cached, new, table, 64, 320, ids[used:], 0)
+    ref["table"][2, :2] = ref["table"][0, :2]  # the only member with tokens behind its first
+    cache = tq.PagedCache(ctx, 7, 1, 320, 64, n_blocks=40, block_table=torch.from_numpy(table))
+    b = buffers(7, sum(new))
+    tq.build_tables(ctx, cache, dev(cached), dev(new), **b, free_list=dev(ids[used:]), free_start=dev([0]),
+                    cu_group=dev(groups), prefix_lens=dev([prefix, 64, prefix]))
+    ctx.check_device_errors()
+    assert np.array_equal(cache.block_table.cpu().numpy(), ref["table"])
+    for k in ("seq_idx", "pos", "slots", "cu_new", "seq_lens"):
+        assert b[k].tolist() == ref[k], k
