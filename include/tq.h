@@ -408,10 +408,11 @@ tq_status tq_decode_attention_shared(
  *              Neither may overlap an input.
  * scale <= 0 means 1/sqrt(d).  No workspace.  Query heads per KV head at most
  * 16.  Scores and sums are fp32; the softmax weights are rounded to bf16 for
- * the product with V.  A NaN or infinity in a token's K or V reaches, besides
- * the queries at and after it, at most those up to 127 positions before it in
- * the same prompt.  A prompt whose bounds are out of range or longer than
- * max_len gets no output and sets the seq_len flag of tq_check_device_errors.
+ * the product with V.  A query with a score of NaN or +inf gets NaN.  A NaN or
+ * infinity in a token's V reaches, besides the queries at and after it, at most
+ * those up to 127 positions before it in the same prompt.  A prompt whose bounds
+ * are out of range or longer than max_len gets no output and sets the seq_len
+ * flag of tq_check_device_errors.  n_tok, n_seqs or max_len of 0 is a no-op.
  */
 tq_status tq_prompt_attention(tq_ctx *ctx, const void *q, const void *k,
                               const void *v, int64_t q_stride,
@@ -495,10 +496,11 @@ tq_status tq_build_tables_words(const void *words);            /* 19 words */
 /*
  * Synchronise `stream`, then report and clear the context's sticky
  * device-side error flags: TQ_OK, or TQ_ERR_DEVICE with a message naming the
- * flags (bit 0: a token outside the cache in tq_quantize, or a paged
- * cache's block-table entry outside [0, n_blocks) in either call; bit 1:
- * seq_len outside [0, max_seq_len] in tq_decode_attention; bit 2: a bounded
- * wait in a kernel expired).
+ * flags (bit 0: a token outside the cache in tq_quantize, a paged cache's
+ * block-table entry outside [0, n_blocks) in any call, a free list that ran out
+ * or rows past n_tok in tq_build_tables; bit 1: a length, or the bounds of a
+ * prompt or a group, outside what its call was given; bit 2: a bounded wait in
+ * a kernel expired).
  */
 tq_status tq_check_device_errors(tq_ctx *ctx, void *stream);
 

@@ -32,11 +32,15 @@
 // so that the scores' A operand takes no shared-memory reads (32 cycles an MMA
 // of N = 64 instead of 50) and the ring has 7 slots instead of 5 (a K tile's load
 // no longer waits for the values of the step before): 540 -> 438 us for 5 prompts
-// of up to 5000 tokens, 16 over 4 heads.
-// Measured: one prompt of 32768 tokens, 32 over 8 heads, d = 128, 7.6 to 7.9 ms
-// (1.11 to 1.16 PFLOP/s, a plain bf16 GEMM sustains 1.40); 17 of up to 4001 tokens
-// 1.23 ms (1.0).  No pipe is full (tensor 49 %, MUFU 37 %, issue 42 %): what bounds
-// it are the hand-overs between the softmax and MMA warps of a row tile.
+// of up to 5000 tokens, 16 over 4 heads, in a loop on one input (whose K and V
+// then stay in L2).
+// Measured on changing inputs: one prompt of 32768 tokens, 32 over 8 heads, d = 128,
+// 7.9 ms (1.11 PFLOP/s, a plain bf16 GEMM sustains 1.40), one of 16384 at 28 over 4
+// heads 1.84 ms (1.05); 17 of up to 4001 tokens 1.43 ms (0.86); d = 256, 5 of up to
+// 5000, 435 us (0.92).  No pipe is full (tensor 47 %, MUFU 36 %, issue 42 %): a long
+// prompt is bound by the hand-overs between the softmax and MMA warps of a row tile,
+// many short ones also by each CTA's start and end, which one CTA per SM leaves
+// uncovered.
 // P is rounded to bf16, V's type (one MMA takes one type for A and B); l is
 // summed in fp32 from the unrounded weights.
 #include <cuda_bf16.h>
@@ -414,8 +418,8 @@ __global__ void __launch_bounds__(PromptCfg<DH, ROWS>::kThreads, PromptCfg<DH, R
         const bool need_p = h >= 0 && h < mine;
         // (one row tile: usually all three are there, and one test of each is
         // quicker than three waits, 373 us against 438 for 5 prompts of up to
-        // 5000 tokens at d = 256; with two row tiles P mostly is not, and the
-        // tests in front of the wait cost 3 %)
+        // 5000 tokens at d = 256 in a loop on one input; with two row tiles P
+        // mostly is not, and the tests in front of the wait cost 3 %)
         uint32_t ready = 0;
         if (NT == 1 && need_v && need_k && need_p)
           ready = test_three(&full[vs], vp, &full[ks], kp, &p_full[i][h & 1], (h >> 1) & 1);

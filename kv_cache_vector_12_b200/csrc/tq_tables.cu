@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesA
 // are resident at once (four per SM): a decode step of up to 512 tokens without
 // groups is a single CTA.  More tokens than resident threads (prompts, whose rows
 // run on in one block) are taken four to a thread: 1.05 M tokens 8.6 us, and 9.7
-// with one to a thread; a step of 32 sequences 3.6 us with four, 2.4 with one.
+// with one to a thread (contiguous, 1.13 M tokens 7.3 us); a step of 32 sequences
+// 3.6 us with four, 2.4 with one.
 int launch_tables(const DeviceParams &p, const tq_cache &c, int32_t *block_table, const int32_t *cached,
                   const int32_t *fresh, const int32_t *free_list, int n_free, const int32_t *free_start,
                   int32_t *free_end, const int32_t *cu_group, const int32_t *prefix, int n_groups, int n_tok,

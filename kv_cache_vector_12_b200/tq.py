@@ -1,7 +1,10 @@
-"""Thin Python binding of ``libtq.so`` (argument marshalling only).
+"""Thin Python binding of ``libtq.so`` (argument checks and marshalling only).
 
 Every function mirrors the C entry point of the same name in ``include/tq.h``;
-every step of the hot path runs in the library's CUDA kernels.  PyTorch is
+every step of the hot path runs in the library's CUDA kernels.  The serving
+operators (build_tables, prompt_attention, decode_attention_shared) compare
+their tensors' sizes, types, layouts and devices with what the call reads and
+writes; the other functions hand their pointers over as they are.  PyTorch is
 used here only to allocate device memory and to hand over stream handles.
 Importing this module loads the library and raises ``ImportError`` if it has
 not been built: there is no fallback.
