@@ -170,3 +170,48 @@ def test_host_tensors_and_other_types_are_refused(tq):
     refused(lambda **kw: tq.decode_attention_shared(ctx, cache, **kw), shared, q=q[:1], seq_lens=_ints(70, 80).long(),
             cu_group=_ints(0), out=out[:2].half(), workspace=ws.cpu(), prefix_lens=_ints(64).cpu())
     assert (out == 7.0).all()
+
+
+def test_all_operators_at_once(tq):
+    """Prompts of both forms, shared decode on tcgen05, tables and appends on five streams: tensor memory, shared memory
+    and the contexts' flags are what they have in common, and every output is the one of the call alone."""
+    from tests.test_gpu_shared import Batch
+    g = torch.Generator().manual_seed(1)
+    heads = lambda n, k, d: torch.randn(n, k, d, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    jobs = []
+    for d, lens in ((64, [200, 3, 77]), (128, [900, 130]), (256, [300, 5])):
+        ctx, n = tq.Context(d, 3, 3, 0, 42), sum(lens)
+        q, k, v = heads(n, 8, d), heads(n, 2, d), heads(n, 2, d)
+        cu, out = _ints(0, *np.cumsum(lens).tolist()), torch.empty_like(q)
+        jobs.append((out, ctx, lambda st, a=(ctx, q, k, v, cu, max(lens)), o=out: tq.prompt_attention(*a, o, stream=st)))
+    b = Batch(tq, [0, 40], [2000], [2000 + s for s in range(40)])
+    ws = tq.alloc_shared_workspace(b.ctx, b.cache, 8, 1, 40, 2000, 60)
+    out, args = torch.empty_like(b.q), (_ints(*b.lens), _ints(0, 40), _ints(2000), 40, 2000, 60)
+    jobs.append((out, b.ctx, lambda st, o=out: tq.decode_attention_shared(b.ctx, b.cache, b.q, *args, o, None, ws,
+                                                                          stream=st)))
+    own = tq.Context(D, 3, 3, 0, 42)
+    cache = tq.Cache(own, 4, H, 1024)
+    rows, fresh, none = heads(3000, H, D), _ints(1000, 900, 800, 300), _ints(0, 0, 0, 0)
+    seq_idx, pos = (torch.empty(3000, dtype=torch.int32, device="cuda") for _ in range(2))
+    first, ends = torch.empty(5, dtype=torch.int32, device="cuda"), torch.empty(4, dtype=torch.int32, device="cuda")
+
+    def append(st):
+        tq.build_tables(own, cache, none, fresh, seq_idx, pos, first, ends, stream=st)
+        tq.quantize(own, cache, rows, rows, seq_idx, pos, stream=st)
+
+    jobs.append((cache.planes["codes_k"], own, append))
+    refs = []
+    for out, _, call in jobs:
+        call(None)
+        torch.cuda.synchronize()
+        refs.append(out.clone())
+        out.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(40):
+        for (_, _, call), st in zip(jobs, streams):
+            call(st)
+    torch.cuda.synchronize()
+    for (out, ctx, _), ref in zip(jobs, refs):
+        ctx.check_device_errors()
+        assert torch.equal(out, ref)
